@@ -365,6 +365,194 @@ const char *mk_last_error(const mk_handle *h);
 /* mk_destroy - free everything the handle owns.  NULL is allowed. */
 void mk_destroy(mk_handle *h);
 
+/*
+ * 8-bit paged K/V caches and the pages of a cache.
+ *
+ * The calls below work on caller-owned device memory and take no handle.  A
+ * sequence s has kv_len[s] = c positions in the cache before a call and
+ * n = row_start[s + 1] - row_start[s] new rows, which take the positions
+ * c .. c + n - 1; position p is row p % page_size of page
+ * d_page_table[s][p / page_size].  They are asynchronous and ordered on
+ * `stream`, allocate nothing, may be captured into a CUDA graph, run on the
+ * device named in their first argument whatever the current device is, and
+ * leave the current device as it was.  Calls that write one cache or the same
+ * page tables must be ordered by the caller, as must calls that share a
+ * workspace.  mk_last_error(NULL) gives the text of the calling thread's last
+ * refusal.  What only the device can see (a page outside the pools, lengths
+ * that do not fit) is recorded in the caller's status words d_status, 4 int32
+ * that the caller zeroes first: {MK_ERR_DEVICE or MK_ERR_OOM, sequence or
+ * entry, its value, which check (MK_CHECK_...)} of one of the failures of the
+ * calls since then; what such a call still does is stated with it.
+ */
+enum { MK_KV8_INT8 = 0, MK_KV8_E4M3 = 1 };   /* codes of an 8-bit cache */
+enum { MK_F32 = 0, MK_BF16 = 1, MK_F16 = 2 }; /* element types of rows */
+enum {
+  MK_CHECK_ROWS = 1,    /* row_start out of order, outside [0, n_rows], or more than max_rows */
+  MK_CHECK_LENGTH = 2,  /* kv_len < 0, or kv_len + n above max_pages * page_size */
+  MK_CHECK_PAGE = 3,    /* page table entry outside [0, n_pages) */
+  MK_CHECK_SEQ = 4,     /* sequence or page number of a list out of range, or named twice */
+  MK_CHECK_IN_USE = 5,  /* fork into a sequence that holds pages */
+  MK_CHECK_FREE = 6     /* fewer free pages than needed (MK_ERR_OOM; value: how many are lacking) */
+};
+
+/* A paged cache in 8 bits.  K and V codes: int8, or e4m3 (no infinities; the
+ * codes 0x7f and 0xff are not used); the value of a code is code * scale, with
+ * one scale for every `block` positions of a (page, layer, kv head). */
+typedef struct {
+  int device;
+  int format;                   /* MK_KV8_INT8 or MK_KV8_E4M3 */
+  int n_layers, n_kv_heads;
+  int head_dim;                 /* D: 64 or 128 */
+  int page_size;                /* P positions per page, a multiple of block */
+  int block;                    /* positions per scale: 16, 32, 64 or 128 */
+  int n_pages;
+  void *d_k, *d_v;              /* [n_pages][n_layers][n_kv_heads][P][D], 16-byte aligned */
+  float *d_k_scale, *d_v_scale; /* [n_pages][n_layers][n_kv_heads][P / block] */
+  int32_t *d_status;            /* 4 status words, or NULL */
+} mk_kv8_cache;
+
+/* Rows [n_rows][heads][head_dim] with contiguous head_dim; base 16-byte
+ * aligned, strides (in elements) whole multiples of 16 bytes. */
+typedef struct {
+  const void *data;
+  int dtype;                    /* MK_F32, MK_BF16 or MK_F16 */
+  int64_t row_stride, head_stride;
+} mk_rows;
+
+/* The sequences of a call and their new rows. */
+typedef struct {
+  int n_seqs;                   /* at least 1 */
+  int n_rows;                   /* rows of the row arrays */
+  int max_rows;                 /* bound on the new rows of one sequence */
+  int max_pages;                /* page table entries per sequence */
+  const int32_t *d_row_start;   /* [n_seqs + 1], or NULL: row s belongs to sequence s (n_rows = n_seqs) */
+  const int32_t *d_kv_len;      /* [n_seqs] positions cached before the new rows */
+  const int32_t *d_page_table;  /* [n_seqs][max_pages]; entries that no position of the call needs may be anything */
+} mk_batch;
+
+/*
+ * mk_kv8_store - quantise the batch's new K and V rows into layer `layer` of
+ * the cache.  For every block that receives rows, with a = max |x| of its new
+ * rows and qmax = 127 (int8) or 448 (e4m3):
+ *   scale = max(a * (1 / qmax), 2^-126), and at least the block's old scale where
+ *   the block holds positions below kv_len[s];
+ *   code = round(x * (1 / scale)) to nearest even, clamped to +-qmax;
+ *   if the scale of a block with earlier positions grew, their codes become
+ *   round(code * (old scale * (1 / scale))).
+ * All in fp32.  If a is not finite the block's scale becomes NaN, its new
+ * codes 0, and every position of it reads as NaN until the block is begun
+ * again by a row at its first position.  Codes and scales of other positions
+ * keep their bytes.  Two sequences of one call must not write one page.
+ * Device checks: a sequence that fails MK_CHECK_ROWS or MK_CHECK_LENGTH is
+ * left out, and so are the rows of a page that fails MK_CHECK_PAGE (with a
+ * row_start out of order, other sequences may be left out as well).
+ * Errors: MK_ERR_ARG, MK_ERR_CUDA.
+ */
+mk_status mk_kv8_store(const mk_kv8_cache *cache, int layer, const mk_rows *k, const mk_rows *v,
+                       const mk_batch *batch, void *stream);
+
+/*
+ * mk_kv8_attention - attention of the batch's new query rows over layer
+ * `layer` of the cache: row i of sequence s sees the positions
+ * 0 .. kv_len[s] + i, its own included (store the call's K/V rows first).
+ * Head h reads kv head h / (n_q_heads / n_kv_heads).  d_out [n_rows][n_q_heads]
+ * [head_dim], contiguous and 16-byte aligned, has the element type of q;
+ * d_lse [n_rows][n_q_heads] (or NULL) receives log(sum(exp(scores))).  Rows
+ * outside every sequence are not written.  Scores, softmax and output are
+ * accumulated in fp32; the products take q as one fp16 term per element
+ * relative to its row's largest power of two (two terms for fp32 rows) and the
+ * probabilities likewise, and the codes exactly.  max_rows is at most
+ * MK_KV8_MAX_ROWS: the call is made for decoding, not for prompts.
+ * Workspace: at least mk_kv8_attention_workspace bytes, 16-byte aligned; its
+ * contents need not be initialised.  Results do not depend on how the work is
+ * spread over time: the same call gives the same bits.
+ * Device checks: the rows of a sequence that fails MK_CHECK_LENGTH,
+ * MK_CHECK_PAGE or has more than max_rows rows become NaN; a sequence whose
+ * row_start is out of order or range is left out.  Errors: MK_ERR_ARG, MK_ERR_CUDA.
+ */
+enum { MK_KV8_MAX_ROWS = 16 };
+mk_status mk_kv8_attention(const mk_kv8_cache *cache, int layer, const mk_rows *q, int n_q_heads,
+                           float scale, void *d_out, float *d_lse, const mk_batch *batch,
+                           void *d_workspace, int64_t workspace_bytes, void *stream);
+
+/* mk_kv8_attention_workspace - bytes of workspace that a call with this cache,
+ * query heads, element type and batch sizes needs (no device memory is read). */
+mk_status mk_kv8_attention_workspace(const mk_kv8_cache *cache, int n_q_heads, int dtype,
+                                     const mk_batch *batch, int64_t *bytes);
+
+/* Pools of pages (of bf16 or 8-bit caches) and who holds which page.  ref[p]
+ * counts the page table entries that name page p; a page with 0 is free.  A
+ * caller begins with every table entry -1 (no page) and every count 0. */
+enum { MK_MAX_POOLS = 8 };
+typedef struct {
+  int device;
+  int n_pages, n_seqs, max_pages, page_size;
+  int n_pools;
+  void *d_pool[MK_MAX_POOLS];         /* pool i: n_pages pages of page_bytes[i] bytes, 4-byte aligned */
+  int64_t page_bytes[MK_MAX_POOLS];   /* multiples of 4 */
+  int32_t *d_page_table;              /* [n_seqs][max_pages] */
+  int32_t *d_ref;                     /* [n_pages] */
+  int32_t *d_status;                  /* 4 status words, or NULL */
+} mk_pages;
+
+/* mk_pages_workspace - bytes of workspace for the calls below with up to n
+ * list entries (16-byte aligned, contents need not be initialised). */
+mk_status mk_pages_workspace(const mk_pages *pages, int n, int64_t *bytes);
+
+/*
+ * mk_pages_fork - sequence d_dst[i] takes the pages of sequence d_src[i]
+ * (shared, counted, not copied) for i < n.  The destinations must differ, hold
+ * no pages and not be a source.  Device checks: a list entry that is out of
+ * range or a destination named twice or as a source (MK_CHECK_SEQ), a
+ * destination that holds pages (MK_CHECK_IN_USE), a source entry outside
+ * [-1, n_pages) (MK_CHECK_PAGE): the call then changes nothing.
+ */
+mk_status mk_pages_fork(const mk_pages *pages, int n, const int32_t *d_src, const int32_t *d_dst,
+                        void *d_workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * mk_pages_free - sequences d_seqs[i], i < n, give their pages back; their
+ * entries become -1.  A sequence may be named twice.  Device checks:
+ * MK_CHECK_SEQ, MK_CHECK_PAGE (the call then changes nothing).
+ */
+mk_status mk_pages_free(const mk_pages *pages, int n, const int32_t *d_seqs, void *d_workspace,
+                        int64_t workspace_bytes, void *stream);
+
+/*
+ * mk_pages_reserve - make the positions kv_len[s] .. kv_len[s] + n_new[s] - 1
+ * of every sequence with n_new[s] > 0 writable.  Of the entries that hold
+ * these positions, those without a page get a free page, and those whose page
+ * is shared are given a free page instead, with the contents copied if the
+ * page holds positions below kv_len[s] -- unless every sequence that shares
+ * the page writes it in this call: then the one with the highest number keeps
+ * it.
+ * Free pages are given lowest number first, in the order of sequence and
+ * entry; pages that this call gives up are not given out by it.  Device
+ * checks: MK_CHECK_LENGTH, MK_CHECK_PAGE, MK_CHECK_FREE (the call then changes
+ * nothing).
+ */
+mk_status mk_pages_reserve(const mk_pages *pages, const int32_t *d_kv_len, const int32_t *d_n_new,
+                           void *d_workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * mk_pages_compact - move the U pages in use to the page numbers 0 .. U - 1:
+ * the i-th page in use with a number >= U moves to the i-th free number < U.
+ * Contents, counts and every table entry follow.  Device check: MK_CHECK_PAGE
+ * (an entry outside [-1, n_pages), or one that names a free page: the call
+ * then changes nothing).
+ */
+mk_status mk_pages_compact(const mk_pages *pages, void *d_workspace, int64_t workspace_bytes,
+                           void *stream);
+
+/*
+ * mk_pages_copy - page d_dst[i] of every pool receives the contents of page
+ * d_src[i], i < n; tables and counts stay.  Device check: MK_CHECK_SEQ (a
+ * number out of range, a destination named twice or as a source: the call
+ * then copies nothing).
+ */
+mk_status mk_pages_copy(const mk_pages *pages, int n, const int32_t *d_src, const int32_t *d_dst,
+                        void *d_workspace, int64_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

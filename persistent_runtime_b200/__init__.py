@@ -27,7 +27,17 @@ EXPORTS = ("mk_plan_graph", "mk_graph_from_edges", "mk_build_graph", "mk_load_we
            "mk_decode_step_noalloc",
            "mk_sync_status", "mk_reset",
            "mk_graph_export", "mk_get_info", "mk_final_hidden", "mk_debug_set_event_count",
-           "mk_set_trace", "mk_set_timeout_us", "mk_last_error", "mk_destroy")
+           "mk_set_trace", "mk_set_timeout_us", "mk_last_error", "mk_destroy",
+           "mk_kv8_store", "mk_kv8_attention", "mk_kv8_attention_workspace",
+           "mk_pages_workspace", "mk_pages_fork", "mk_pages_free", "mk_pages_reserve",
+           "mk_pages_compact", "mk_pages_copy")
+
+MK_KV8_INT8, MK_KV8_E4M3 = 0, 1
+MK_F32, MK_BF16, MK_F16 = 0, 1, 2
+MK_KV8_MAX_ROWS, MK_MAX_POOLS = 16, 8
+# status word 3 of the calls on 8-bit caches and pages: which check failed
+CHECKS = {1: "row_start", 2: "kv_len", 3: "page table entry", 4: "sequence or page of a list",
+          5: "fork into a sequence that holds pages", 6: "free pages"}
 
 
 class MkError(RuntimeError):
@@ -85,6 +95,30 @@ class Info(ctypes.Structure):
         ("weight_bytes", ctypes.c_int64), ("act_bytes", ctypes.c_int64)]
 
 
+class Kv8Cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("device", "format", "n_layers", "n_kv_heads", "head_dim",
+                                            "page_size", "block", "n_pages")] + [
+        (n, ctypes.c_void_p) for n in ("d_k", "d_v", "d_k_scale", "d_v_scale", "d_status")]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class Batch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("n_seqs", "n_rows", "max_rows", "max_pages")] + [
+        (n, ctypes.c_void_p) for n in ("d_row_start", "d_kv_len", "d_page_table")]
+
+
+class Pages(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("device", "n_pages", "n_seqs", "max_pages", "page_size",
+                                            "n_pools")] + [
+        ("d_pool", ctypes.c_void_p * MK_MAX_POOLS), ("page_bytes", ctypes.c_int64 * MK_MAX_POOLS),
+        ("d_page_table", ctypes.c_void_p), ("d_ref", ctypes.c_void_p),
+        ("d_status", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -119,6 +153,16 @@ def lib():
         "mk_set_timeout_us": ([vp, ctypes.c_uint], st),
         "mk_last_error": ([vp], ctypes.c_char_p),
         "mk_destroy": ([vp], None),
+        "mk_kv8_store": ([vp, i32, vp, vp, vp, vp], st),
+        "mk_kv8_attention": ([vp, i32, vp, i32, ctypes.c_float, vp, vp, vp, vp, ctypes.c_int64, vp],
+                             st),
+        "mk_kv8_attention_workspace": ([vp, i32, i32, vp, vp], st),
+        "mk_pages_workspace": ([vp, i32, vp], st),
+        "mk_pages_fork": ([vp, i32, vp, vp, vp, ctypes.c_int64, vp], st),
+        "mk_pages_free": ([vp, i32, vp, vp, ctypes.c_int64, vp], st),
+        "mk_pages_reserve": ([vp, vp, vp, vp, ctypes.c_int64, vp], st),
+        "mk_pages_compact": ([vp, vp, ctypes.c_int64, vp], st),
+        "mk_pages_copy": ([vp, i32, vp, vp, vp, ctypes.c_int64, vp], st),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -346,3 +390,279 @@ class Megakernel:
 
     def set_timeout_us(self, us: int):
         _check(lib().mk_set_timeout_us(self._h, us), self._h)
+
+
+# ----------------------------------------------------------------------------
+# 8-bit paged caches and the pages of a cache (no handle, caller-owned tensors)
+# ----------------------------------------------------------------------------
+def _refuse(why: str):
+    raise MkError(MK_ERR_ARG, why)
+
+
+class _Status:
+    """The device status words of a cache or of a set of pages."""
+
+    def _new_status(self):
+        import torch
+        self.status = torch.zeros(4, dtype=torch.int32, device=self.device)
+
+    def sync_status(self):
+        """Waits for the device's work; returns (status, [status, which, value, check]), status
+        0 = ok, and leaves the words as they are until reset()."""
+        import torch
+        torch.cuda.synchronize(self.device)
+        d = self.status.tolist()
+        return d[0], d
+
+    def reset(self):
+        self.status.zero_()
+
+    def check(self):
+        """Raises MkError for a failure that the device has recorded."""
+        rc, d = self.sync_status()
+        if rc != 0:
+            raise MkError(rc, f"the device refused: {CHECKS.get(d[3], d[3])} (entry {d[1]}, "
+                              f"value {d[2]})")
+
+    def _int32(self, t, n, what):
+        """Address of a contiguous int32 tensor of n entries (n None: any) on this device."""
+        if t.dtype is not self._i32 or t.device != self.device or not t.is_contiguous():
+            _refuse(f"{what} must be a contiguous int32 tensor on {self.device}")
+        if n is not None and t.numel() != n:
+            _refuse(f"{what} must have {n} entries")
+        return t.data_ptr()
+
+    def _stream(self, stream):
+        if stream is None:
+            return self._current_stream(self.device).cuda_stream
+        return stream.cuda_stream
+
+    def _bind(self, device):
+        import torch
+        self.device = device
+        self._i32 = torch.int32
+        self._current_stream = torch.cuda.current_stream
+        self._empty = torch.empty
+        self._uint8 = torch.uint8
+        self._lib = lib()
+        if device.type != "cuda":
+            _refuse(f"tensors must be on a CUDA device, not {device}")
+
+
+class KV8Cache(_Status):
+    """A paged K/V cache in 8 bits with a scale for every `block` positions of a (page, layer,
+    kv head), on the caller's tensors:
+
+    k, v              int8 or float8_e4m3fn [n_pages][n_layers][n_kv_heads][page_size][head_dim]
+    k_scale, v_scale  float32 [n_pages][n_layers][n_kv_heads][page_size / block]
+
+    The pages belong to sequences as in Megakernel.decode_steps_paged: position p of sequence s
+    is row p % page_size of page page_table[s][p // page_size]."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        self._bind(k.device)
+        formats = {torch.int8: MK_KV8_INT8, torch.float8_e4m3fn: MK_KV8_E4M3}
+        if k.dim() != 5 or k.dtype not in formats:
+            _refuse("k must be int8 or float8_e4m3fn [n_pages][n_layers][n_kv_heads][page_size]"
+                    "[head_dim]")
+        if k_scale.dim() != 4 or tuple(k_scale.shape[:3]) != tuple(k.shape[:3]) \
+                or k_scale.shape[3] < 1 or k.shape[3] % k_scale.shape[3]:
+            _refuse("k_scale must be [n_pages][n_layers][n_kv_heads][page_size / block]")
+        if v.shape != k.shape or v.dtype != k.dtype or v_scale.shape != k_scale.shape:
+            _refuse("k and v differ in shape or type")
+        if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+            _refuse("scales must be float32")
+        for t in (k, v, k_scale, v_scale):
+            if t.device != k.device or not t.is_contiguous():
+                _refuse("k, v and their scales must be contiguous and on one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._new_status()
+        n_pages, n_layers, n_kv_heads, page_size, head_dim = k.shape
+        self.n_pages, self.n_layers, self.n_kv_heads = n_pages, n_layers, n_kv_heads
+        self.page_size, self.head_dim = page_size, head_dim
+        self.block = page_size // k_scale.shape[3]
+        self._c = Kv8Cache(k.device.index, formats[k.dtype], n_layers, n_kv_heads, head_dim,
+                           page_size, self.block, n_pages, k.data_ptr(), v.data_ptr(),
+                           k_scale.data_ptr(), v_scale.data_ptr(), self.status.data_ptr())
+        self._dtypes = {torch.float32: MK_F32, torch.bfloat16: MK_BF16, torch.float16: MK_F16}
+        self._workspaces = {}
+        self._ref = ctypes.byref(self._c)
+        _check(self._lib.mk_kv8_attention_workspace(self._ref, n_kv_heads, MK_BF16, ctypes.byref(
+            Batch(1, 1, 1, 1, None, self.status.data_ptr(), self.status.data_ptr())),
+            ctypes.byref(ctypes.c_int64())))  # the library's own checks of the cache
+
+    @classmethod
+    def empty(cls, n_pages, n_layers, n_kv_heads, head_dim, page_size=64, block=64, dtype=None,
+              device="cuda"):
+        """A cache on new tensors; dtype torch.int8 (default) or torch.float8_e4m3fn."""
+        import torch
+        if block < 1 or page_size % block:
+            _refuse("page_size must be a multiple of block")
+        shape = (n_pages, n_layers, n_kv_heads, page_size, head_dim)
+        scales = shape[:3] + (page_size // block,)
+        dtype = torch.int8 if dtype is None else dtype
+        return cls(*(torch.empty(shape, dtype=dtype, device=device) for _ in range(2)),
+                   *(torch.ones(scales, dtype=torch.float32, device=device) for _ in range(2)))
+
+    def pools(self):
+        """The tensors whose first dimension are pages, for PagePool."""
+        return [self.k, self.v, self.k_scale, self.v_scale]
+
+    def _rows(self, x, n_heads, what):
+        if x.dim() != 3 or (n_heads and x.shape[1] != n_heads) or x.shape[2] != self.head_dim \
+                or x.stride(2) != 1:
+            _refuse(f"{what} must be [rows][{n_heads or 'heads'}][{self.head_dim}] with contiguous "
+                    "head_dim")
+        if x.dtype not in self._dtypes or x.device != self.device:
+            _refuse(f"{what} must be float32, bfloat16 or float16 on {self.device}")
+        return Rows(x.data_ptr(), self._dtypes[x.dtype], x.stride(0), x.stride(1))
+
+    def _batch(self, page_table, kv_len, row_start, n_rows, max_rows):
+        if page_table.dim() != 2 or page_table.shape[1] < 1:
+            _refuse("page_table must be [n_seqs][max_pages]")
+        n, max_pages = page_table.shape
+        start = None if row_start is None else self._int32(row_start, n + 1, "row_start")
+        if row_start is None and n_rows != n:
+            _refuse("without row_start there is one row per sequence")
+        return Batch(n, n_rows, max_rows, max_pages, start, self._int32(kv_len, n, "kv_len"),
+                     self._int32(page_table, None, "page_table"))
+
+    def store(self, layer, k, v, page_table, kv_len, row_start=None, stream=None):
+        """mk_kv8_store: quantise the new rows k, v [n_rows][n_kv_heads][head_dim] (float32,
+        bfloat16 or float16) and append them to layer `layer`; rows row_start[s] to
+        row_start[s + 1] - 1 (row s without row_start) go to the positions from kv_len[s]."""
+        n_rows = k.shape[0]
+        if v.shape != k.shape or v.dtype != k.dtype:
+            _refuse("k and v differ in shape or type")
+        rk, rv = self._rows(k, self.n_kv_heads, "k"), self._rows(v, self.n_kv_heads, "v")
+        b = self._batch(page_table, kv_len, row_start, n_rows, max(1, n_rows))
+        if n_rows:
+            _check(self._lib.mk_kv8_store(self._ref, layer, ctypes.byref(rk), ctypes.byref(rv),
+                                          ctypes.byref(b), self._stream(stream)))
+
+    def attention(self, layer, q, page_table, kv_len, row_start=None, max_rows=None, scale=None,
+                  out=None, return_lse=False, stream=None):
+        """mk_kv8_attention: q [n_rows][n_q_heads][head_dim]; row i of sequence s sees the
+        positions 0 to kv_len[s] + i.  max_rows bounds the rows of one sequence (1 without
+        row_start; at most MK_KV8_MAX_ROWS).  Returns the output in q's type, and with
+        return_lse also the float32 log-sum-exp [n_rows][n_q_heads]."""
+        n_rows, n_heads = q.shape[0], q.shape[1] if q.dim() == 3 else 0
+        rq = self._rows(q, 0, "q")
+        if max_rows is None:
+            if row_start is not None:
+                _refuse("max_rows is needed with row_start")
+            max_rows = 1
+        b = self._batch(page_table, kv_len, row_start, n_rows, max_rows)
+        if out is None:
+            out = self._empty((n_rows, n_heads, self.head_dim), dtype=q.dtype, device=self.device)
+        elif out.shape != q.shape or out.dtype != q.dtype or out.device != self.device \
+                or not out.is_contiguous():
+            _refuse("out must be contiguous, with the shape, type and device of q")
+        lse = self._empty((n_rows, n_heads), dtype=self.k_scale.dtype, device=self.device) \
+            if return_lse else None
+        if scale is None:
+            scale = self.head_dim ** -0.5
+        key = (n_heads, rq.dtype, b.n_seqs, max_rows, b.max_pages)
+        size = self._workspaces.get(key)
+        if size is None:
+            bytes_ = ctypes.c_int64()
+            _check(self._lib.mk_kv8_attention_workspace(self._ref, n_heads, rq.dtype,
+                                                        ctypes.byref(b), ctypes.byref(bytes_)))
+            size = self._workspaces[key] = bytes_.value
+        if n_rows:
+            # a workspace of its own for every call: calls on other streams and
+            # captured graphs do not meet in it
+            ws = self._empty(size, dtype=self._uint8, device=self.device) if size else None
+            _check(self._lib.mk_kv8_attention(
+                self._ref, layer, ctypes.byref(rq), n_heads, scale, out.data_ptr(), _ptr(lse),
+                ctypes.byref(b), _ptr(ws), size, self._stream(stream)))
+            if ws is not None and stream is not None:
+                ws.record_stream(stream)
+        return (out, lse) if return_lse else out
+
+
+class PagePool(_Status):
+    """The pages of a cache and who holds them, on the caller's tensors:
+
+    page_table  int32 [n_seqs][max_pages], -1 = no page
+    ref_count   int32 [n_pages], page table entries that name the page
+    pools       tensors whose first dimension are the pages: the K and V pools of
+                Megakernel.decode_steps_paged, or KV8Cache.pools()"""
+
+    def __init__(self, page_table, ref_count, page_size, pools):
+        self._bind(page_table.device)
+        if page_table.dim() != 2 or ref_count.dim() != 1:
+            _refuse("page_table must be [n_seqs][max_pages] and ref_count [n_pages]")
+        if len(pools) > MK_MAX_POOLS:
+            _refuse(f"more than {MK_MAX_POOLS} pools")
+        self.page_table, self.ref_count, self.page_size = page_table, ref_count, page_size
+        self.pools = list(pools)
+        self._new_status()
+        n_pages = ref_count.numel()
+        p = self._c = Pages(page_table.device.index, n_pages, page_table.shape[0],
+                            page_table.shape[1], page_size, len(pools))
+        for i, x in enumerate(self.pools):
+            if x.dim() < 1 or x.shape[0] != n_pages or x.device != self.device \
+                    or not x.is_contiguous():
+                _refuse(f"pool {i} must be contiguous, on {self.device}, with {n_pages} pages")
+            p.d_pool[i] = x.data_ptr()
+            p.page_bytes[i] = x.numel() // n_pages * x.element_size()
+        p.d_page_table = self._int32(page_table, None, "page_table")
+        p.d_ref = self._int32(ref_count, None, "ref_count")
+        p.d_status = self.status.data_ptr()
+        self._ref = ctypes.byref(p)
+        self._sizes = {}
+        self._workspace(0)
+
+    @classmethod
+    def empty(cls, n_seqs, max_pages, page_size, pools):
+        """Nobody holds a page yet."""
+        import torch
+        device = pools[0].device
+        return cls(torch.full((n_seqs, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(pools[0].shape[0], dtype=torch.int32, device=device), page_size,
+                   pools)
+
+    def _workspace(self, n):
+        size = self._sizes.get(n)
+        if size is None:
+            b = ctypes.c_int64()
+            _check(self._lib.mk_pages_workspace(self._ref, n, ctypes.byref(b)))
+            size = self._sizes[n] = b.value
+        return size
+
+    def _call(self, fn, n, args, stream):
+        size = self._workspace(n)
+        ws = self._empty(size, dtype=self._uint8, device=self.device)
+        _check(fn(self._ref, *args, ws.data_ptr(), size, self._stream(stream)))
+        if stream is not None:
+            ws.record_stream(stream)
+
+    def fork(self, src, dst, stream=None):
+        """mk_pages_fork: sequences dst take (and share) the pages of sequences src."""
+        n = src.numel()
+        self._call(self._lib.mk_pages_fork, n, (n, self._int32(src, None, "src"),
+                                                self._int32(dst, n, "dst")), stream)
+
+    def free(self, seqs, stream=None):
+        """mk_pages_free: the sequences give their pages back."""
+        n = seqs.numel()
+        self._call(self._lib.mk_pages_free, n, (n, self._int32(seqs, None, "seqs")), stream)
+
+    def reserve(self, kv_len, n_new, stream=None):
+        """mk_pages_reserve: pages that only their sequence holds under the positions kv_len[s]
+        to kv_len[s] + n_new[s] - 1 of every sequence."""
+        n = self._c.n_seqs
+        self._call(self._lib.mk_pages_reserve, 0, (self._int32(kv_len, n, "kv_len"),
+                                                   self._int32(n_new, n, "n_new")), stream)
+
+    def compact(self, stream=None):
+        """mk_pages_compact: the pages in use move to the lowest page numbers."""
+        self._call(self._lib.mk_pages_compact, 0, (), stream)
+
+    def copy(self, src, dst, stream=None):
+        """mk_pages_copy: pages dst of every pool take the contents of pages src."""
+        n = src.numel()
+        self._call(self._lib.mk_pages_copy, n, (n, self._int32(src, None, "src"),
+                                                self._int32(dst, n, "dst")), stream)

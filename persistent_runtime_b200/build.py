@@ -12,7 +12,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmk.so")
-SOURCES = ["mk_worker.cu", "mk_api.cpp", "tgraph.cpp", "mk_static.cu"]
+SOURCES = ["mk_worker.cu", "mk_api.cpp", "tgraph.cpp", "mk_static.cu", "kv8_store.cu",
+           "kv8_attention.cu", "kv_pages.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -13,6 +14,7 @@
 #include <string>
 #include <vector>
 
+#include "kv8.cuh"
 #include "runtime.cuh"
 #include "tgraph.hpp"
 
@@ -685,6 +687,81 @@ mk_status mk_load_weights(mk_handle *h, const mk_weights *w, void *stream) {
 }
 
 }  // extern "C"
+
+// The calls without a handle (8-bit caches, pages): errors and shared checks.
+mk_status mk::ops_fail(mk_status s, const char *call, const char *text) noexcept {
+  try {
+    g_last_error = std::string(call) + ": " + text;
+  } catch (...) {  // no memory for the text: the status still says what happened
+  }
+  return s;
+}
+
+mk_status mk::ops_cuda_fail(cudaError_t e, const char *call) noexcept {
+  return ops_fail(MK_ERR_CUDA, call, cudaGetErrorString(e));
+}
+
+mk_status mk::ops_workspace(const char *call, const void *workspace, int64_t have,
+                            int64_t need) noexcept {
+  if (need <= 0) return MK_OK;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15))
+    return ops_fail(MK_ERR_ARG, call, "the workspace is null or not 16-byte aligned");
+  if (have < need) {
+    char text[96];
+    std::snprintf(text, sizeof(text), "workspace of %lld bytes, %lld are needed", (long long)have,
+                  (long long)need);
+    return ops_fail(MK_ERR_ARG, call, text);
+  }
+  return MK_OK;
+}
+
+int mk::sm_count(int device) {
+  static std::atomic<int> known[64];
+  const bool keep = device >= 0 && device < 64;
+  int n = keep ? known[device].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return 1;
+  if (keep) known[device].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+const char *mk::check_kv8_cache(const mk_kv8_cache *c, int layer) {
+  if (!c) return "null cache";
+  if (c->device < 0) return "bad device";
+  if (c->format != MK_KV8_INT8 && c->format != MK_KV8_E4M3) return "unknown format";
+  if (c->n_layers < 1 || c->n_kv_heads < 1 || c->n_pages < 1) return "empty cache";
+  if (c->n_kv_heads > 65535) return "more than 65535 kv heads";
+  if (layer < 0 || layer >= c->n_layers) return "layer out of range";
+  if (c->head_dim != 64 && c->head_dim != 128) return "head_dim must be 64 or 128";
+  if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128)
+    return "block must be 16, 32, 64 or 128";
+  if (c->page_size < c->block || c->page_size % c->block) return "page_size must be a multiple of block";
+  if (!c->d_k || !c->d_v || !c->d_k_scale || !c->d_v_scale) return "null buffer";
+  if ((reinterpret_cast<uintptr_t>(c->d_k) | reinterpret_cast<uintptr_t>(c->d_v)) & 15)
+    return "K/V codes must be 16-byte aligned";
+  return nullptr;
+}
+
+const char *mk::check_batch(const mk_batch *b, int page_size) {
+  if (!b) return "null batch";
+  if (b->n_seqs < 1 || b->n_rows < 0 || b->max_rows < 1 || b->max_pages < 1)
+    return "n_seqs, max_rows and max_pages must be at least 1";
+  if (b->n_seqs > (1 << 24)) return "more than 2^24 sequences";
+  if ((int64_t)b->max_pages * page_size >= (1ll << 31) - 65536) return "sequences of 2^31 positions are not supported";
+  if (!b->d_kv_len || !b->d_page_table) return "null lengths or page table";
+  if (!b->d_row_start && b->n_rows != b->n_seqs && b->n_rows != 0)
+    return "without row_start there is one row per sequence";
+  return nullptr;
+}
+
+const char *mk::check_rows(const mk_rows *r) {
+  if (!r || !r->data) return "null rows";
+  if (r->dtype < MK_F32 || r->dtype > MK_F16) return "element type must be MK_F32, MK_BF16 or MK_F16";
+  if (reinterpret_cast<uintptr_t>(r->data) & 15) return "rows must be 16-byte aligned";
+  const int64_t unit = r->dtype == MK_F32 ? 4 : 8;
+  if (r->row_stride % unit || r->head_stride % unit) return "row strides must be multiples of 16 bytes";
+  return nullptr;
+}
 
 namespace {
 

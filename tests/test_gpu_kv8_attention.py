@@ -1,0 +1,215 @@
+"""mk_kv8_attention against softmax attention in 64 bits on the dequantised cache."""
+import numpy as np
+import pytest
+
+import kv8_ref as ref
+from kv8_ref import dev, make_table, torch
+
+pytestmark = pytest.mark.gpu
+
+CASES = [
+    # q heads, kv heads, dim, page, block, format, dtype, cached, new rows
+    (4, 2, 64, 64, 16, "int8", "bfloat16", [0], [1]),
+    (4, 2, 64, 64, 64, "e4m3", "float32", [1], [1]),
+    (16, 8, 128, 64, 64, "int8", "float16", [511, 0, 15, 16, 31, 32], [1] * 6),
+    (32, 8, 128, 64, 32, "int8", "float32", [700, 3, 1200], [1] * 3),
+    (32, 8, 128, 16, 16, "e4m3", "bfloat16", [1000, 17, 0, 300], [2, 0, 5, 1]),
+    (16, 1, 128, 128, 128, "int8", "bfloat16", [900, 40], [1, 1]),
+    (40, 2, 64, 48, 16, "e4m3", "float16", [100, 600], [3, 1]),
+    (8, 8, 128, 256, 128, "e4m3", "float32", [2000, 255], [4, 16]),
+    (6, 2, 64, 32, 32, "int8", "bfloat16", [5000], [16]),
+    (24, 3, 128, 64, 16, "int8", "float32", [650, 1], [7, 2]),
+]
+
+
+def setup(case, seed, layers=2):
+    Hq, H, D, P, T, fmt, dtype, cached, new = case
+    t = torch()
+    cached, new = np.array(cached), np.array(new)
+    table, n_pages = make_table(cached + new, P, seed=seed)
+    host = ref.Cache(n_pages, layers, H, D, P, T, fmt, seed)
+    start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = t.from_numpy(np.random.default_rng(seed + 7).standard_normal((start[-1], Hq, D)).astype(np.float32))
+    q = q.to(getattr(t, dtype))
+    return host, q, table, cached, new, start
+
+
+def check(got, lse, host, layer, q, table, cached, start, scale, dtype):
+    out, want_lse, tol, tol_lse = host.attention(layer, q.float().numpy(), table, cached, start, scale, dtype)
+    err = np.abs(got.double().cpu().numpy() - out)
+    worst = np.unravel_index(np.argmax(err / tol), err.shape)
+    assert np.all(err <= tol), (worst, err[worst], tol[worst])
+    err = np.abs(lse.double().cpu().numpy() - want_lse)
+    assert np.all(err <= tol_lse), (err.max(), tol_lse.max())
+
+
+@pytest.mark.parametrize("case", CASES, ids=[f"{c[5]}-{c[6]}-{c[0]}x{c[1]}-d{c[2]}-p{c[3]}-b{c[4]}" for c in CASES])
+def test_against_64_bits(case):
+    Hq, H, D, P, T, fmt, dtype, cached, new = case
+    host, q, table, cached, new, start = setup(case, 11)
+    cache = host.device()
+    for scale in (None, 0.31):
+        out, lse = cache.attention(1, q.cuda(), dev(table), dev(cached.astype(np.int32)),
+                                   row_start=None if (new == 1).all() else dev(start),
+                                   max_rows=int(new.max()), scale=scale, return_lse=True)
+        cache.check()
+        check(out, lse, host, 1, q, table, cached, start, scale or D ** -0.5, dtype)
+
+
+def test_many_uneven_sequences():
+    rng = np.random.default_rng(1)
+    lens = rng.integers(0, 700, 300)  # more sequences than threads of a block
+    case = (8, 2, 64, 32, 32, "int8", "bfloat16", lens, np.ones(300, int))
+    host, q, table, cached, new, start = setup(case, 12, layers=1)
+    cache = host.device()
+    out, lse = cache.attention(0, q.cuda(), dev(table), dev(cached.astype(np.int32)), return_lse=True)
+    cache.check()
+    check(out, lse, host, 0, q, table, cached, start, 64 ** -0.5, "bfloat16")
+
+
+def test_large_and_small_scores_and_scales():
+    """Scores of +-hundreds (one position takes all), blocks whose scales differ by 2^60."""
+    case = (4, 2, 128, 64, 16, "int8", "float32", [333], [1])
+    for k_size, v_size in ((50.0, 1.0), (1e-12, 2.0 ** 30)):
+        host, q, table, cached, new, start = setup(case, 13)
+        host.scales[0] *= np.float32(k_size)
+        host.scales[1][:, :, :, ::2] *= np.float32(v_size)
+        host.scales[1][:, :, :, 1::2] /= np.float32(v_size)
+        cache = host.device()
+        out, lse = cache.attention(1, q.cuda(), dev(table), dev(cached.astype(np.int32)), return_lse=True)
+        check(out, lse, host, 1, q, table, cached, start, 128 ** -0.5, "float32")
+
+
+def test_what_lies_behind_the_end_does_not_matter():
+    """Codes (NaN ones too), scales and table entries past the last position, and a later
+    row's block that reads as NaN, do not reach the rows that do not see them."""
+    for fmt in ("int8", "e4m3"):
+        case = (4, 2, 64, 64, 16, fmt, "bfloat16", [70, 41], [3, 2])
+        host, q, table, cached, new, start = setup(case, 14)
+        clean = host.device().attention(1, q.cuda(), dev(table), dev(cached.astype(np.int32)),
+                                        row_start=dev(start), max_rows=3)
+        for s in range(2):
+            n = int(cached[s] + new[s])
+            for which in range(2):
+                host.codes[which][table[s][(n - 1) // 64], :, :, n % 64:] = 0xff
+                host.scales[which][table[s][(n - 1) // 64], :, :, (n - 1) % 64 // 16 + 1:] = np.nan
+        cache = host.device()
+        table[:, -1] = 1 << 30
+        got = cache.attention(1, q.cuda(), dev(table), dev(cached.astype(np.int32)),
+                              row_start=dev(start), max_rows=3)
+        cache.check()
+        assert torch().equal(got, clean)
+    # rows 0 and 1 of sequence 1 (positions 46, 47) do not see the block of position 48
+    case = (4, 2, 64, 64, 16, "int8", "float32", [10, 46], [1, 4])
+    host, q, table, cached, new, start = setup(case, 15)
+    host.scales[0][table[1][0], :, :, 3] = np.nan
+    host.scales[1][table[1][0], :, :, 3] = np.nan
+    cache = host.device()
+    out = cache.attention(1, q.cuda(), dev(table), dev(cached.astype(np.int32)), row_start=dev(start),
+                          max_rows=4).cpu().numpy()
+    assert np.isfinite(out[:3]).all() and np.isnan(out[3:]).all()
+
+
+def test_rows_with_nan_or_infinity_stay_by_themselves():
+    case = (8, 2, 128, 64, 64, "int8", "bfloat16", [200, 90], [2, 1])
+    host, q, table, cached, new, start = setup(case, 16)
+    cache = host.device()
+    args = (dev(table), dev(cached.astype(np.int32)))
+    clean = cache.attention(1, q.cuda(), *args, row_start=dev(start), max_rows=2)
+    q2 = q.clone()
+    q2[1, 3, 7] = float("nan")
+    q2[2, 0, 0] = float("inf")
+    q2[0, 5] = 0.0
+    got = cache.attention(1, q2.cuda(), *args, row_start=dev(start), max_rows=2)
+    t = torch()
+    assert bool(t.isnan(got[1, 3]).all()) and bool(t.isnan(got[2, 0]).all())
+    keep = t.ones(3, 8, dtype=t.bool)
+    keep[1, 3] = keep[2, 0] = keep[0, 5] = False
+    assert t.equal(got[keep.cuda()], clean[keep.cuda()])
+    mean = host.rows(1, 1, table[0], 201).mean(0)[5 // 4]  # a zero query weighs all positions alike
+    np.testing.assert_allclose(got[0, 5].float().cpu().numpy(), mean, rtol=0, atol=2.0 ** -7 * np.abs(mean).max())
+
+
+def test_strides_bounds_and_repeats():
+    t = torch()
+    case = (8, 4, 64, 32, 16, "e4m3", "float16", [300, 20, 0], [2, 0, 3])
+    host, q, table, cached, new, start = setup(case, 17)
+    cache = host.device()
+    args = (dev(table), dev(cached.astype(np.int32)))
+    want = cache.attention(1, q.cuda(), *args, row_start=dev(start), max_rows=3)
+    packed = t.zeros(7, 20, 64, dtype=t.float16, device="cuda")
+    packed[:5, 3:11] = q.cuda()
+    out = t.full((7, 8, 64), 7.0, dtype=t.float16, device="cuda")
+    got = cache.attention(1, packed[:, 3:11], *args, row_start=dev(start), max_rows=16, out=out)
+    cache.check()
+    assert got is out and t.equal(out[:5], want) and bool((out[5:] == 7).all())
+    for _ in range(3):
+        assert t.equal(cache.attention(1, q.cuda(), *args, row_start=dev(start), max_rows=3), want)
+
+
+def test_device_checks_make_the_sequence_nan():
+    import persistent_runtime_b200 as prb
+    t = torch()
+    case = (4, 2, 64, 32, 16, "int8", "bfloat16", [600, 700, 40], [1, 1, 1])
+    host, q, table, cached, new, start = setup(case, 18)
+    cache = host.device()
+    d_len = dev(cached.astype(np.int32))
+    clean, clean_lse = cache.attention(1, q.cuda(), dev(table), d_len, return_lse=True)
+    cap = table.shape[1] * 32
+    for what, check_id in (("page", 3), ("negative", 2), ("long", 2)):
+        tab, lens = table.copy(), cached.astype(np.int32).copy()
+        if what == "page":
+            tab[1, 9] = -1
+        else:
+            lens[1] = -1 if what == "negative" else cap
+        out, lse = cache.attention(1, q.cuda(), dev(tab), dev(lens), return_lse=True)
+        rc, d = cache.sync_status()
+        assert rc == prb.MK_ERR_DEVICE and d[1] == 1 and d[3] == check_id
+        assert t.equal(out[[0, 2]], clean[[0, 2]]) and bool(t.isnan(out[1]).all())
+        assert t.equal(lse[[0, 2]], clean_lse[[0, 2]]) and bool(t.isnan(lse[1]).all())
+        cache.reset()
+    # more rows than max_rows
+    q3 = t.cat([q, q]).cuda()
+    out = cache.attention(1, q3, dev(table), dev(np.array([5, 6, 7], np.int32)),
+                          row_start=dev(np.array([0, 1, 5, 6], np.int32)), max_rows=2)
+    assert cache.sync_status()[1][3] == 1
+    assert bool(t.isnan(out[1:5]).all()) and not bool(t.isnan(out[[0, 5]]).any())
+
+
+def test_streams_graphs_and_two_calls_at_once():
+    t = torch()
+    case = (16, 8, 128, 64, 64, "int8", "bfloat16", [3000, 2500], [1, 1])
+    host, q, table, cached, new, start = setup(case, 19)
+    cache = host.device()
+    a, d_table, d_len = q.cuda(), dev(table), dev(cached.astype(np.int32))
+    b = (a * 0.5).contiguous()
+    want = [cache.attention(1, x, d_table, d_len) for x in (a, b)]
+    side = [t.cuda.Stream(), t.cuda.Stream()]
+    t.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for st, x in zip(side, (a, b)):
+            with t.cuda.stream(st):
+                got.append(cache.attention(1, x, d_table, d_len))
+    got.append(cache.attention(1, a, d_table, d_len, stream=side[0]))
+    t.cuda.synchronize()
+    for i, x in enumerate(got[:-1]):
+        assert t.equal(x, want[i % 2])
+    assert t.equal(got[-1], want[0])
+    graphs = []
+    for x in (a, b):
+        g = t.cuda.CUDAGraph()
+        with t.cuda.graph(g):
+            out = cache.attention(1, x, d_table, d_len)
+        graphs.append((g, out))
+    for _ in range(5):
+        for (g, out), st in zip(graphs, side):
+            out.zero_()
+            t.cuda.synchronize()
+        for (g, out), st in zip(graphs, side):
+            with t.cuda.stream(st):
+                g.replay()
+        t.cuda.synchronize()
+        for (g, out), w in zip(graphs, want):
+            assert t.equal(out, w)
+    cache.check()

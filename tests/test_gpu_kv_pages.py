@@ -1,0 +1,259 @@
+"""The page calls against a sequential restatement: tables, counts and contents, exactly."""
+import numpy as np
+import pytest
+
+import kv8_ref as ref
+from kv8_ref import dev, torch
+
+pytestmark = pytest.mark.gpu
+
+
+class Host:
+    """Tables, counts and pools on the host; a page's contents are a number in every pool."""
+
+    def __init__(self, n_seqs, max_pages, page, n_pages, seed=0):
+        self.page, self.n_pages = page, n_pages
+        self.table = np.full((n_seqs, max_pages), -1, np.int32)
+        self.ref = np.zeros(n_pages, np.int32)
+        rng = np.random.default_rng(seed)
+        # 16-byte pages, pages with a 4-byte rest, pages longer than a copy step
+        self.pools = [rng.integers(0, 1 << 30, (n_pages, w)).astype(np.int32) for w in (4, 7, 8200 + 1024, 9001)]
+
+    def hold(self, s, pages):
+        self.table[s, :len(pages)] = pages
+        np.add.at(self.ref, pages, 1)
+
+    def device(self):
+        import persistent_runtime_b200 as prb
+        return prb.PagePool(dev(self.table), dev(self.ref), self.page, [dev(p) for p in self.pools])
+
+    def fork(self, src, dst):
+        for s, d in zip(src, dst):
+            self.table[d] = self.table[s]
+            for p in self.table[s]:
+                if p >= 0:
+                    self.ref[p] += 1
+
+    def free(self, seqs):
+        for s in seqs:
+            for p in self.table[s]:
+                if p >= 0:
+                    self.ref[p] -= 1
+            self.table[s] = -1
+
+    def reserve(self, kv_len, n_new):
+        free = [p for p in range(self.n_pages) if self.ref[p] == 0]
+        P = self.page
+        entries = [(s, j) for s in range(len(kv_len)) if n_new[s] > 0
+                   for j in range(kv_len[s] // P, -(-(kv_len[s] + n_new[s]) // P))]
+        writers = {}
+        for s, j in entries:
+            if self.table[s, j] >= 0:
+                writers.setdefault(self.table[s, j], []).append((s, j))
+        start = self.ref.copy()
+        for s, j in entries:
+            p = self.table[s, j]
+            if p >= 0 and (start[p] == 1 or (len(writers[p]) == start[p] and writers[p][-1] == (s, j))):
+                continue
+            fresh = free.pop(0)
+            self.table[s, j], self.ref[fresh] = fresh, 1
+            if p >= 0:
+                self.ref[p] -= 1
+                if j * P < kv_len[s]:
+                    for pool in self.pools:
+                        pool[fresh] = pool[p]
+
+    def compact(self):
+        used = [p for p in range(self.n_pages) if self.ref[p] > 0]
+        U = len(used)
+        to = dict(zip([p for p in used if p >= U], [p for p in range(U) if self.ref[p] == 0]))
+        for a, b in to.items():
+            self.ref[b], self.ref[a] = self.ref[a], 0
+            for pool in self.pools:
+                pool[b] = pool[a]
+        self.table = np.array([[to.get(p, p) for p in row] for row in self.table], np.int32)
+
+
+def same(host, pages):
+    pages.check()
+    np.testing.assert_array_equal(pages.page_table.cpu().numpy(), host.table)
+    np.testing.assert_array_equal(pages.ref_count.cpu().numpy(), host.ref)
+    for got, want in zip(pages.pools, host.pools):
+        np.testing.assert_array_equal(got.cpu().numpy(), want)
+    named = np.bincount(host.table[host.table >= 0], minlength=host.n_pages)
+    np.testing.assert_array_equal(host.ref, named)
+
+
+def i32(x):
+    return dev(np.array(x, np.int32))
+
+
+@pytest.mark.parametrize("n_seqs,max_pages,page,n_pages,seed", [(3, 4, 16, 20, 0), (40, 9, 64, 300, 1),
+                                                              (700, 5, 16, 5000, 2), (9, 2000, 16, 40000, 3)])
+def test_a_life_of_sequences(n_seqs, max_pages, page, n_pages, seed):
+    """Reserve, fork, write on, free and compact in random order, as a server does."""
+    rng = np.random.default_rng(seed)
+    host = Host(n_seqs, max_pages, page, n_pages, seed)
+    if n_pages > 10000:  # contents of a few words are enough here
+        host.pools = host.pools[:2]
+    pages = host.device()
+    lens = np.zeros(n_seqs, np.int64)
+    for step in range(12):
+        n_new = rng.integers(0, 3 * page, n_seqs) * (rng.random(n_seqs) < 0.7)
+        n_new = np.minimum(n_new, max_pages * page - lens)
+        need = sum(-(-(int(c) + int(n)) // page) - int(c) // page for c, n in zip(lens, n_new) if n > 0)
+        if need <= (host.ref == 0).sum():
+            host.reserve(lens.tolist(), n_new.tolist())
+            pages.reserve(i32(lens), i32(n_new))
+            same(host, pages)
+            lens += n_new
+        empty = np.flatnonzero(lens == 0)
+        full = np.flatnonzero(lens > 0)
+        if len(empty) and len(full):
+            k = rng.integers(1, len(empty) + 1)
+            dst = rng.permutation(empty)[:k]
+            src = rng.choice(full, k)
+            host.fork(src, dst)
+            pages.fork(i32(src), i32(dst))
+            same(host, pages)
+            lens[dst] = lens[src]
+            # forked sequences may be cut back: their next rows land in shared pages
+            lens[dst] -= rng.integers(0, 1 + lens[dst])
+            for s in dst:
+                lens[s] = max(lens[s], 1)
+        gone = np.flatnonzero(rng.random(n_seqs) < 0.3)
+        if len(gone):
+            twice = np.concatenate([gone, gone[:2]])  # a sequence may be named twice
+            host.free(gone)
+            pages.free(i32(twice))
+            same(host, pages)
+            lens[gone] = 0
+        if step % 3 == 2:
+            host.compact()
+            pages.compact()
+            same(host, pages)
+            used = int((host.ref > 0).sum())
+            assert (host.ref[:used] > 0).all()
+
+
+def test_all_holders_write_the_last_keeps_the_page():
+    host = Host(5, 3, 16, 12)
+    host.hold(0, [7, 3])
+    pages = host.device()
+    host.fork([0, 0], [2, 4])
+    pages.fork(i32([0, 0]), i32([2, 4]))
+    host.reserve([20, 0, 20, 0, 20], [1, 0, 1, 0, 1])
+    pages.reserve(i32([20, 0, 20, 0, 20]), i32([1, 0, 1, 0, 1]))
+    same(host, pages)
+    assert host.table[4, 1] == 3 and host.table[0, 1] != 3 and host.ref[3] == 1
+    # only one of two holders writes: the other keeps the page
+    host.fork([2], [1])
+    pages.fork(i32([2]), i32([1]))
+    host.reserve([0, 21, 0, 0, 0], [0, 1, 0, 0, 0])
+    pages.reserve(i32([0, 21, 0, 0, 0]), i32([0, 1, 0, 0, 0]))
+    same(host, pages)
+
+
+def test_copy():
+    host = Host(1, 1, 16, 50)
+    pages = host.device()
+    src, dst = [3, 3, 9, 49], [0, 48, 4, 17]
+    pages.copy(i32(src), i32(dst))
+    for pool in host.pools:
+        pool[dst] = pool[src]
+    same(host, pages)
+    pages.copy(i32([]), i32([]))
+    same(host, pages)
+
+
+def test_failures_change_nothing():
+    import persistent_runtime_b200 as prb
+
+    def fails(call, check, code=prb.MK_ERR_DEVICE):
+        call()
+        rc, d = pages.sync_status()
+        assert rc == code and d[3] == check, (rc, d)
+        pages.reset()
+        same(host, pages)
+        return d
+
+    host = Host(4, 3, 16, 8)
+    host.hold(0, [5, 2])
+    host.hold(1, [6])
+    pages = host.device()
+    fails(lambda: pages.fork(i32([0, 1]), i32([2, 2])), 4)
+    fails(lambda: pages.fork(i32([0, 2]), i32([2, 3])), 4)
+    fails(lambda: pages.fork(i32([0]), i32([4])), 4)
+    fails(lambda: pages.fork(i32([-1]), i32([2])), 4)
+    fails(lambda: pages.fork(i32([0]), i32([1])), 5)
+    fails(lambda: pages.free(i32([0, 4])), 4)
+    fails(lambda: pages.copy(i32([0]), i32([8])), 4)
+    fails(lambda: pages.copy(i32([0, 1]), i32([3, 3])), 4)
+    fails(lambda: pages.copy(i32([0, 1]), i32([1, 3])), 4)
+    fails(lambda: pages.reserve(i32([0, 0, -1, 0]), i32([0, 0, 1, 0])), 2)
+    fails(lambda: pages.reserve(i32([0, 0, 40, 0]), i32([0, 0, 9, 0])), 2)
+    d = fails(lambda: pages.reserve(i32([32, 16, 0, 0]), i32([16, 32, 48, 1])), 6, prb.MK_ERR_OOM)
+    assert d[2] == 1 + 2 + 3 + 1 - 5
+    pages.reserve(i32([32, 16, 0, 0]), i32([16, 32, 0, 32]))  # exactly the free ones
+    host.reserve([32, 16, 0, 0], [16, 32, 0, 32])
+    same(host, pages)
+    for bad, calls in ((8, ("fork", "free", "reserve", "compact")), (-2, ("fork", "free", "reserve", "compact"))):
+        pages.page_table[0, 2] = bad
+        host.table[0, 2] = bad
+        for name in calls:
+            {"fork": lambda: pages.fork(i32([0]), i32([2])), "free": lambda: pages.free(i32([1, 0])),
+             "reserve": lambda: pages.reserve(i32([32, 0, 0, 0]), i32([1, 0, 0, 0])),
+             "compact": pages.compact}[name]()
+            rc, d = pages.sync_status()
+            assert rc == prb.MK_ERR_DEVICE and d[3] == 3
+            pages.reset()
+            np.testing.assert_array_equal(pages.page_table.cpu().numpy(), host.table)
+            np.testing.assert_array_equal(pages.ref_count.cpu().numpy(), host.ref)
+    pages.page_table[0, 2] = 0
+    pages.ref_count[0] = 0  # an entry that names a free page
+    pages.compact()
+    assert pages.sync_status()[1][3] == 3
+
+
+def test_captured_calls_and_another_stream():
+    t = torch()
+    host = Host(6, 4, 16, 30)
+    host.hold(0, [20, 21, 29])
+    host.hold(1, [11])
+    pages = host.device()
+    src, dst, lens, new = i32([0, 0]), i32([2, 3]), i32([40, 3, 40, 40, 0, 0]), i32([1, 1, 1, 1, 0, 20])
+    gone = i32([0])
+    pages.fork(src, dst)  # warm-up outside the capture, taken back
+    pages.free(dst)
+    table0, ref0 = pages.page_table.clone(), pages.ref_count.clone()
+    pools0 = [p.clone() for p in pages.pools]
+    t.cuda.synchronize()
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        pages.fork(src, dst)
+        pages.reserve(lens, new)
+        pages.free(gone)
+        pages.compact()
+    host.fork([0, 0], [2, 3])
+    host.reserve([40, 3, 40, 40, 0, 0], [1, 1, 1, 1, 0, 20])
+    host.free([0])
+    host.compact()
+    for _ in range(3):
+        pages.page_table.copy_(table0)
+        pages.ref_count.copy_(ref0)
+        for p, p0 in zip(pages.pools, pools0):
+            p.copy_(p0)
+        g.replay()
+        same(host, pages)
+    st = t.cuda.Stream()
+    st.wait_stream(t.cuda.current_stream())
+    pages.page_table.copy_(table0)
+    pages.ref_count.copy_(ref0)
+    for p, p0 in zip(pages.pools, pools0):
+        p.copy_(p0)
+    t.cuda.synchronize()
+    pages.fork(src, dst, stream=st)
+    pages.reserve(lens, new, stream=st)
+    pages.free(gone, stream=st)
+    pages.compact(stream=st)
+    same(host, pages)
