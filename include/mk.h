@@ -480,6 +480,26 @@ mk_status mk_kv8_attention(const mk_kv8_cache *cache, int layer, const mk_rows *
 mk_status mk_kv8_attention_workspace(const mk_kv8_cache *cache, int n_q_heads, int dtype,
                                      const mk_batch *batch, int64_t *bytes);
 
+/*
+ * mk_decode_step_kv8 - mk_decode_step_perop over an 8-bit paged cache: the
+ * same task bodies, launched one grid per operator, with the attention
+ * operator replaced by the per-head norms and RoPE, mk_kv8_store and
+ * mk_kv8_attention.  The cache's layers, kv heads and head_dim must be the
+ * handle's; d_page_table is int32 [batch][max_pages] with max_pages *
+ * page_size >= kv_capacity; the handle may be built for contiguous or paged
+ * K/V.  Tokens, lengths, logits and device-side errors (in the handle's
+ * status word) are those of mk_decode_step; additionally a page table entry
+ * out of range under a position of the step makes the step write nothing.
+ * Workspace: mk_decode_step_kv8_workspace bytes, 16-byte aligned, not to be
+ * used by another call that runs at the same time.
+ */
+mk_status mk_decode_step_kv8(mk_handle *h, const int32_t *d_tokens_in, int32_t *d_tokens_out,
+                             int32_t *d_kv_len, const mk_kv8_cache *cache,
+                             const int32_t *d_page_table, int max_pages, float *d_logits,
+                             void *d_workspace, int64_t workspace_bytes, void *stream);
+mk_status mk_decode_step_kv8_workspace(mk_handle *h, const mk_kv8_cache *cache, int max_pages,
+                                       int64_t *bytes);
+
 /* Pools of pages (of bf16 or 8-bit caches) and who holds which page.  ref[p]
  * counts the page table entries that name page p; a page with 0 is free.  A
  * caller begins with every table entry -1 (no page) and every count 0. */

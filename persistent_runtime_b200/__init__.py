@@ -30,7 +30,8 @@ EXPORTS = ("mk_plan_graph", "mk_graph_from_edges", "mk_build_graph", "mk_load_we
            "mk_set_trace", "mk_set_timeout_us", "mk_last_error", "mk_destroy",
            "mk_kv8_store", "mk_kv8_attention", "mk_kv8_attention_workspace",
            "mk_pages_workspace", "mk_pages_fork", "mk_pages_free", "mk_pages_reserve",
-           "mk_pages_compact", "mk_pages_copy")
+           "mk_pages_compact", "mk_pages_copy", "mk_decode_step_kv8",
+           "mk_decode_step_kv8_workspace")
 
 MK_KV8_INT8, MK_KV8_E4M3 = 0, 1
 MK_F32, MK_BF16, MK_F16 = 0, 1, 2
@@ -157,6 +158,8 @@ def lib():
         "mk_kv8_attention": ([vp, i32, vp, i32, ctypes.c_float, vp, vp, vp, vp, ctypes.c_int64, vp],
                              st),
         "mk_kv8_attention_workspace": ([vp, i32, i32, vp, vp], st),
+        "mk_decode_step_kv8": ([vp, vp, vp, vp, vp, vp, i32, vp, vp, ctypes.c_int64, vp], st),
+        "mk_decode_step_kv8_workspace": ([vp, vp, i32, vp], st),
         "mk_pages_workspace": ([vp, i32, vp], st),
         "mk_pages_fork": ([vp, i32, vp, vp, vp, ctypes.c_int64, vp], st),
         "mk_pages_free": ([vp, i32, vp, vp, ctypes.c_int64, vp], st),
@@ -353,6 +356,25 @@ class Megakernel:
         _check(lib().mk_decode_step_noalloc(self._h, _ptr(tokens_in), _ptr(tokens_out),
                                             _ptr(kv_len), _ptr(k_cache), _ptr(v_cache),
                                             _ptr(logits), _stream_ptr(stream)), self._h)
+
+    def decode_step_kv8(self, tokens_in, tokens_out, kv_len, cache, page_table, logits=None,
+                        stream=None):
+        """One step, a grid per operator, over an 8-bit paged cache (a KV8Cache with this
+        model's layers, kv heads and head_dim) and its int32 page table [batch][max_pages]."""
+        import torch
+        if page_table.dim() != 2 or page_table.shape[0] != self.w.batch \
+                or page_table.dtype != torch.int32 or not page_table.is_contiguous():
+            _refuse(f"page_table must be a contiguous int32 tensor [{self.w.batch}][max_pages]")
+        size = ctypes.c_int64()
+        max_pages = page_table.shape[1]
+        _check(lib().mk_decode_step_kv8_workspace(self._h, cache._ref, max_pages,
+                                                  ctypes.byref(size)), self._h)
+        ws = torch.empty(size.value, dtype=torch.uint8, device=cache.device)
+        _check(lib().mk_decode_step_kv8(self._h, _ptr(tokens_in), _ptr(tokens_out), _ptr(kv_len),
+                                        cache._ref, page_table.data_ptr(), max_pages, _ptr(logits),
+                                        ws.data_ptr(), size.value, _stream_ptr(stream)), self._h)
+        if stream is not None:
+            ws.record_stream(stream)
 
     def sync_status(self, stream=None):
         """Returns (status, detail[4]); status 0 = ok."""

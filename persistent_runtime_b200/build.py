@@ -13,7 +13,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmk.so")
 SOURCES = ["mk_worker.cu", "mk_api.cpp", "tgraph.cpp", "mk_static.cu", "kv8_store.cu",
-           "kv8_attention.cu", "kv_pages.cu"]
+           "kv8_attention.cu", "kv_pages.cu", "kv8_step.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -48,6 +48,14 @@ const char *check_kv8_cache(const mk_kv8_cache *c, int layer);
 const char *check_batch(const mk_batch *b, int page_size);
 const char *check_rows(const mk_rows *r);
 
+// The launches of the two calls, for arguments that have been checked; with
+// `gate` they do nothing once *gate (on the device) is not 0.
+cudaError_t kv8_store_launch(const mk_kv8_cache &cache, int layer, const mk_rows &k, const mk_rows &v,
+                             const mk_batch &batch, const int32_t *gate, cudaStream_t stream);
+cudaError_t kv8_attention_launch(const mk_kv8_cache &cache, int layer, const mk_rows &q, int n_q_heads,
+                                 float scale, void *out, float *lse, const mk_batch &batch,
+                                 void *workspace, const int32_t *gate, cudaStream_t stream);
+
 #ifdef __CUDACC__
 // ---------------------------------------------------------------------------
 // Device side
@@ -95,6 +103,10 @@ __device__ __forceinline__ SeqRows seq_rows(const mk_batch &b, int page_size, in
   if (q.n > 0 && (q.c < 0 || (int64_t)q.c + q.n > (int64_t)b.max_pages * page_size))
     q.bad = MK_CHECK_LENGTH;
   return q;
+}
+
+__device__ __forceinline__ bool gated(const int32_t *gate) {
+  return gate && *(volatile const int32_t *)gate != 0;
 }
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -76,6 +76,7 @@ struct AttnArgs {
   int4 *head;     // [CTAs][2] the cut pair that begins in each CTA
   float *ml;      // [2 CTAs][rows][2] max, sum of the partial results
   float *part;    // [2 CTAs][rows][D] their unnormalised outputs
+  const int32_t *gate;
 };
 
 constexpr int group_rows(int mode) { return mode == kRows16 ? 16 : 8; }
@@ -616,6 +617,7 @@ template <int D, int FMT, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) kv8_attention_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_trigger();  // the merge launch may get ready; it waits for this grid's end
+  if (gated(a.gate)) return;
   if (a.pair_mode) {
     const int g = blockIdx.x % a.groups, rest = blockIdx.x / a.groups;
     const int hk = rest % a.c.n_kv_heads, s = rest / a.c.n_kv_heads;
@@ -708,6 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attention_kernel(const __grid
 template <int D, int RG>
 __global__ void __launch_bounds__(D) kv8_merge_kernel(const __grid_constant__ AttnArgs a) {
   pdl_wait();
+  if (gated(a.gate)) return;
   const int c0 = blockIdx.x;
   const int4 cut = a.head[2 * c0];
   if (cut.x < 0) return;
@@ -808,6 +811,39 @@ const char *check_heads(const mk_kv8_cache *c, int n_q_heads, int dtype, const m
 }
 
 }  // namespace
+
+cudaError_t kv8_attention_launch(const mk_kv8_cache &cache, int layer, const mk_rows &q, int n_q_heads,
+                                 float scale, void *out, float *lse, const mk_batch &batch,
+                                 void *workspace, const int32_t *gate, cudaStream_t stream) {
+  const AttnPlan p = plan_of(cache, batch, n_q_heads, q.dtype);
+  AttnArgs a{};
+  a.c = cache;
+  a.b = batch;
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.layer = layer;
+  a.n_q_heads = n_q_heads;
+  a.rep = n_q_heads / cache.n_kv_heads;
+  a.scale = scale;
+  a.block_log2 = __builtin_ctz((unsigned)cache.block);
+  a.pair_mode = p.pair_mode;
+  a.groups = p.groups;
+  a.gate = gate;
+  if (p.bytes > 0) {
+    const int rg = group_rows(p.mode);
+    char *w = static_cast<char *>(workspace);
+    a.head = reinterpret_cast<int4 *>(w);
+    a.ml = reinterpret_cast<float *>(w + 32ll * p.ctas);
+    a.part = a.ml + 4ll * rg * p.ctas;
+  }
+  if (cache.head_dim == 128)
+    return cache.format == MK_KV8_INT8 ? launch<128, MK_KV8_INT8>(a, p, stream)
+                                       : launch<128, MK_KV8_E4M3>(a, p, stream);
+  return cache.format == MK_KV8_INT8 ? launch<64, MK_KV8_INT8>(a, p, stream)
+                                     : launch<64, MK_KV8_E4M3>(a, p, stream);
+}
+
 }  // namespace mk
 
 extern "C" mk_status mk_kv8_attention_workspace(const mk_kv8_cache *cache, int n_q_heads, int dtype,
@@ -842,32 +878,8 @@ extern "C" mk_status mk_kv8_attention(const mk_kv8_cache *cache, int layer, cons
   if (ws != MK_OK) return ws;
   DeviceGuard guard(cache->device);
   if (guard.error() != cudaSuccess) return ops_cuda_fail(guard.error(), call);
-  AttnArgs a{};
-  a.c = *cache;
-  a.b = *batch;
-  a.q = *q;
-  a.out = d_out;
-  a.lse = d_lse;
-  a.layer = layer;
-  a.n_q_heads = n_q_heads;
-  a.rep = n_q_heads / cache->n_kv_heads;
-  a.scale = scale;
-  a.block_log2 = __builtin_ctz((unsigned)cache->block);
-  a.pair_mode = p.pair_mode;
-  a.groups = p.groups;
-  if (p.bytes > 0) {
-    const int rg = group_rows(p.mode);
-    char *w = static_cast<char *>(d_workspace);
-    a.head = reinterpret_cast<int4 *>(w);
-    a.ml = reinterpret_cast<float *>(w + 32ll * p.ctas);
-    a.part = a.ml + 4ll * rg * p.ctas;
-  }
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (cache->head_dim == 128)
-    e = cache->format == MK_KV8_INT8 ? launch<128, MK_KV8_INT8>(a, p, st) : launch<128, MK_KV8_E4M3>(a, p, st);
-  else
-    e = cache->format == MK_KV8_INT8 ? launch<64, MK_KV8_INT8>(a, p, st) : launch<64, MK_KV8_E4M3>(a, p, st);
+  const cudaError_t e = kv8_attention_launch(*cache, layer, *q, n_q_heads, scale, d_out, d_lse, *batch,
+                                             d_workspace, nullptr, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return ops_cuda_fail(e, call);
   return MK_OK;
 }

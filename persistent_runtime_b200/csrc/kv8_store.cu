@@ -27,6 +27,7 @@ struct StoreArgs {
   mk_batch b;
   mk_rows x[2];  // K, V
   int layer;
+  const int32_t *gate;
 };
 
 // Eight row elements as fp32.
@@ -96,6 +97,7 @@ __device__ __forceinline__ void decode8(uint2 q, float (&y)[8]) {
 // PASSES x blockDim.x octets of 8 elements make one block of T x D elements.
 template <int FMT, int DT, int PASSES>
 __global__ void __launch_bounds__(256) kv8_store_kernel(const __grid_constant__ StoreArgs a) {
+  if (gated(a.gate)) return;
   const int T = a.c.block, P = a.c.page_size, D = a.c.head_dim;
   const int slot = blockIdx.x, h = blockIdx.y, which = blockIdx.z;
   // the last sequence with f(s) <= slot
@@ -216,6 +218,14 @@ cudaError_t launch_store(const StoreArgs &a, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t kv8_store_launch(const mk_kv8_cache &cache, int layer, const mk_rows &k, const mk_rows &v,
+                             const mk_batch &batch, const int32_t *gate, cudaStream_t stream) {
+  const StoreArgs a{cache, batch, {k, v}, layer, gate};
+  return cache.format == MK_KV8_INT8 ? launch_store<MK_KV8_INT8>(a, stream)
+                                     : launch_store<MK_KV8_E4M3>(a, stream);
+}
+
 }  // namespace mk
 
 extern "C" mk_status mk_kv8_store(const mk_kv8_cache *cache, int layer, const mk_rows *k,
@@ -230,10 +240,8 @@ extern "C" mk_status mk_kv8_store(const mk_kv8_cache *cache, int layer, const mk
   if (why) return ops_fail(MK_ERR_ARG, "mk_kv8_store", why);
   DeviceGuard guard(cache->device);
   if (guard.error() != cudaSuccess) return ops_cuda_fail(guard.error(), "mk_kv8_store");
-  StoreArgs a{*cache, *batch, {*k, *v}, layer};
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = cache->format == MK_KV8_INT8 ? launch_store<MK_KV8_INT8>(a, st)
-                                                     : launch_store<MK_KV8_E4M3>(a, st);
+  const cudaError_t e = kv8_store_launch(*cache, layer, *k, *v, *batch, nullptr,
+                                         static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return ops_cuda_fail(e, "mk_kv8_store");
   return MK_OK;
 }
