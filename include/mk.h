@@ -458,10 +458,12 @@ mk_status mk_kv8_store(const mk_kv8_cache *cache, int layer, const mk_rows *k, c
  * Head h reads kv head h / (n_q_heads / n_kv_heads).  d_out [n_rows][n_q_heads]
  * [head_dim], contiguous and 16-byte aligned, has the element type of q;
  * d_lse [n_rows][n_q_heads] (or NULL) receives log(sum(exp(scores))).  Rows
- * outside every sequence are not written.  Scores, softmax and output are
- * accumulated in fp32; the products take q as one fp16 term per element
- * relative to its row's largest power of two (two terms for fp32 rows) and the
- * probabilities likewise, and the codes exactly.  max_rows is at most
+ * outside every sequence are not written.  Codes enter the products exactly,
+ * sums and softmax are fp32 (int8 products: exact integers).  A query element
+ * enters with an error of at most 2^-21 of its row's largest (int8) or 2^-12
+ * of itself (e4m3; fp32 rows 2^-23), a probability with 2^-17 of the largest of
+ * its chunk of 32 positions (int8; fp32 rows 2^-24) or 2^-12 of itself (e4m3;
+ * fp32 rows 2^-22).  max_rows is at most
  * MK_KV8_MAX_ROWS: the call is made for decoding, not for prompts.
  * Workspace: at least mk_kv8_attention_workspace bytes, 16-byte aligned; its
  * contents need not be initialised.  Results do not depend on how the work is

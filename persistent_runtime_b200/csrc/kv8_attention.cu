@@ -3,30 +3,38 @@
 //
 // Mathematics.  For the query rows r of one kv head (rep heads x n new tokens)
 // and the positions p of a sequence:  x_pr = f_r sk_p (k_p . q'_r) with the
-// codes k_p as they are, q' = q 2^-e in fp16 (e from the row's largest
-// element), f_r = scale log2(e) 2^e and sk_p the scale of p's block; an online
-// softmax in base 2 over chunks of kChunk positions; o_r = sum over blocks of
-// sv (sum over the block's p of P_pr v_p), so that codes and probabilities
-// meet in the tensor cores and the block's scale multiplies an fp32 partial
-// sum.  P carries a factor 2^14, which keeps fp16 normal down to 2^-28 of the
-// largest probability and cancels against the sum.
+// codes k_p as they are, q' the row over a power of two, f_r = scale log2(e) /
+// that factor and sk_p the scale of p's block; softmax in base 2 over chunks of
+// kChunk positions, each relative to its own maximum; o_r = sum over blocks of
+// sv w (sum over the block's p of P_pr v_p), where w brings the chunk to the
+// running maximum.  Codes and probabilities meet in the tensor cores; scales
+// multiply fp32 sums only, so their range does not matter.
+//   int8: codes are MMA operands as they lie in memory.  q' is an integer of
+//   at most 127 2^14, three signed 7-bit digits; P an integer of at most 65535,
+//   two unsigned 8-bit digits (fp32 rows: 2^23, three); the sums are exact.
+//   e4m3: codes become fp16 (exactly), q' is one fp16 number (fp32 rows: two,
+//   11 bits apart), P likewise, times 2^14, which keeps fp16 normal down to
+//   2^-28 of the chunk's maximum.
 //
 // What bounds it: the cache is read once, one byte per element, and every
 // element takes part in 2 x rows multiply-adds, far below the tensor rate for
 // the rows of a decode step: the bound is HBM.  CUDA cores would need rows + 1
 // instructions per byte (at 4 heads per kv head that alone is the SM's issue
-// rate at the HBM rate), so both products run on mma.sync m16n8k16 (fp16 in,
-// fp32 accumulate) with the positions (QK) and the head's dims (PV) as the 16
+// rate at the HBM rate), so both products run on mma.sync (m16n8k32 int8,
+// m16n8k16 fp16) with the positions (QK) and the head's dims (PV) as the 16
 // rows and 8 query rows as columns: the rows of a decode step fill one column
-// tile, where the 128-row tile of tcgen05 would be 15/16 empty and would need
-// the codes expanded into shared memory first.
+// tile, where the 128-row tile of tcgen05 would be 15/16 empty.
 //
-// Layout.  The sum over dims may take the dims in any order, so a lane feeds
-// its QK fragments from the 16 bytes it loaded itself; for PV a lane holds 16
-// (D / 8) dims of four positions.  A lane therefore consumes exactly the bytes
-// that it copied: every warp runs its own ring of kStages chunks filled by
-// cp.async with no barrier, and shared memory reads are conflict-free whatever
-// the page layout.  Positions past the end are filled with zeros by the copy.
+// Layout.  Every warp copies its own chunks with cp.async, K and V into a slot
+// each, and refills a slot as soon as it has consumed it: no barriers between
+// warps.  A warp instruction copies 512 consecutive bytes; copies in the order
+// in which the fragments need the bytes (64-byte halves of rows, 16-byte
+// columns) reach 4.8 TB/s on a B200 where consecutive ones reach 6.5.  The
+// pieces are exchanged on the way in so that fragment reads are free of bank
+// conflicts.  The sum over dims may take them in any order, so a lane's QK
+// fragments are the words of the 16 bytes it reads; for PV a lane reads D / 8
+// dims of four positions and transposes bytes.  Positions past the end are
+// filled with zeros by the copy.
 //
 // Work split.  The (sequence, kv head, row group) pairs, each with
 // ceil(length / kChunk) chunks, lie end to end on one line that the grid cuts
@@ -41,20 +49,17 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kv8.cuh"
 
 namespace mk {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 32;            // positions of a warp's step
 constexpr int kTiles = kChunk / 16;   // 16-position MMA tiles of a chunk
-constexpr int kStages = 3;            // chunks in a warp's ring
 constexpr int kPairChunks = 16;       // longest pair (in chunks) that one CTA takes whole
 constexpr int kMinUnits = 4;          // shortest piece (in chunks) of the cut line
-constexpr float kPShift = 14.0f;      // log2 of the factor that P carries
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // How the query rows fill the MMA columns: 8 rows of a 16-bit type, 16 rows of
@@ -81,13 +86,51 @@ struct AttnArgs {
 
 constexpr int group_rows(int mode) { return mode == kRows16 ? 16 : 8; }
 
-// Shared memory of a warp's ring stage: K codes, V codes, K and V scales.
-__host__ __device__ constexpr int stage_bytes(int D) { return 2 * kChunk * D + 32; }
-__host__ __device__ constexpr int ring_bytes(int D) { return kWarps * kStages * stage_bytes(D); }
-__host__ __device__ constexpr int merge_bytes(int D, int rows) { return kWarps * rows * (D + 4) * 4; }
-__host__ __device__ constexpr int smem_bytes(int D, int mode) {
-  return (ring_bytes(D) > merge_bytes(D, group_rows(mode)) ? ring_bytes(D)
-                                                           : merge_bytes(D, group_rows(mode)));
+// Warps of a CTA and CTAs per SM: as many as their registers allow.
+__host__ __device__ constexpr int n_warps(int, int mode) { return mode == kRows8F32 ? 4 : 8; }
+__host__ __device__ constexpr int n_ctas(int, int mode) { return mode == kRows8F32 ? 2 : 1; }
+
+// Terms of a query element in the MMAs (int8: three signed 7-bit digits, fp16:
+// one or, for fp32 rows, two numbers) and of a probability (8-bit digits; fp16
+// numbers).
+__host__ __device__ constexpr int q_terms(int fmt, int mode) {
+  return fmt == MK_KV8_INT8 ? 3 : mode == kRows8F32 ? 2 : 1;
+}
+__host__ __device__ constexpr int p_terms(int fmt, int mode) {
+  return (fmt == MK_KV8_INT8 ? 2 : 1) + (mode == kRows8F32 ? 1 : 0);
+}
+
+// log2 of the factor that P carries, relative to its chunk's maximum: int8, 16
+// bits (the maximum is 65535) or 24 (2^23); fp16: normal down to 2^-28.
+__host__ __device__ constexpr float p_log2(int fmt, int mode) {
+  return fmt != MK_KV8_INT8 ? 14.0f : mode == kRows8F32 ? 23.0f : 15.99997798605f;
+}
+
+// Shared memory: for each warp a slot for a chunk's K codes and scales and one
+// for V (later the warps' results), then the query rows' terms.
+__host__ __device__ constexpr int slot_bytes(int D) { return kChunk * D + 16; }
+__host__ __device__ constexpr int q_offset(int D, int mode) {
+  const int ring = n_warps(D, mode) * 2 * slot_bytes(D);
+  const int merge = n_warps(D, mode) * group_rows(mode) * (D + 4) * 4;
+  return ring > merge ? ring : merge;
+}
+__host__ __device__ constexpr int smem_bytes(int D, int fmt, int mode) {
+  return q_offset(D, mode) + q_terms(fmt, mode) * group_rows(mode) * D * (fmt == MK_KV8_INT8 ? 1 : 2);
+}
+
+// Codes of a chunk in a slot: as in the cache, but with the eight 16-byte
+// pieces of every 128-byte line exchanged by swizzle(line), which differs in
+// bit 2 for the two lines (D = 128) that eight lanes read for QK and in bits
+// 1-2 for the four that they read for PV: both are free of bank conflicts.
+template <int D>
+__device__ __forceinline__ int swizzle(int line) {
+  return D == 128 ? (line & 6) ^ ((line & 1) << 2) : (line & 3) * 2;
+}
+// Byte of a slot that holds byte `at` (a multiple of 8) of row `row`.
+template <int D>
+__device__ __forceinline__ int slot_at(int row, int at) {
+  const int byte = row * D + at, line = byte >> 7;
+  return line * 128 + ((((byte >> 4) & 7) ^ swizzle<D>(line)) << 4) + (byte & 15);
 }
 
 template <int BYTES>
@@ -112,6 +155,26 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                       uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_s8u8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_s8u8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k16.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0));
+}
+
 // 8 x 8 b16 matrix across the warp, transposed.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
@@ -130,59 +193,31 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ uint32_t hsub2_bits(uint32_t a, uint32_t b) {
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
-  return *reinterpret_cast<const uint32_t *>(&r);
+// Codes to fp16 pairs, exactly: word w (4 e4m3 codes) -> (code 0, code 1), (code 2, code 3).
+__device__ __forceinline__ void expand_e4m3(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
-// Codes to fp16 pairs, exactly.  int8: 0x6400 | (code ^ 0x80) is the fp16
-// number 1024 + 128 + code, from which 1152 is taken away again.
-// Word w (4 codes) -> (code 0, code 1), (code 2, code 3).
-template <int FMT>
-__device__ __forceinline__ void expand(uint32_t w, uint32_t &lo, uint32_t &hi) {
-  if constexpr (FMT == MK_KV8_INT8) {
-    w ^= 0x80808080u;
-    lo = hsub2_bits(__byte_perm(w, 0x64646464u, 0x4140), 0x64806480u);
-    hi = hsub2_bits(__byte_perm(w, 0x64646464u, 0x4342), 0x64806480u);
-  } else {
-    asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-  }
-}
-
-// Words a, b (4 codes of two positions) -> (a_i, b_i) for i = 0 .. 3.
-template <int FMT>
-__device__ __forceinline__ void expand_pairs(uint32_t a, uint32_t b, uint32_t (&h)[4]) {
-  const uint32_t p = __byte_perm(a, b, 0x5140), q = __byte_perm(a, b, 0x7362);
-  expand<FMT>(p, h[0], h[1]);
-  expand<FMT>(q, h[2], h[3]);
-}
-
-__device__ __forceinline__ void load_q16(const mk_rows &q, int64_t at, float (&x)[16]) {
+// N (2 or 4) consecutive elements.
+template <int N>
+__device__ __forceinline__ void load_row(const mk_rows &q, int64_t at, float (&x)[N]) {
   if (q.dtype == MK_F32) {
-    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(q.data) + at);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = p[i];
-      x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+    for (int i = 0; i < N; i += 2) {
+      const float2 v = *reinterpret_cast<const float2 *>(static_cast<const float *>(q.data) + at + i);
+      x[i] = v.x;
+      x[i + 1] = v.y;
     }
   } else {
-    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(q.data) + at);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 v = p[i];
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float2 f;
-        if (q.dtype == MK_BF16)
-          f = make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u));
-        else
-          f = __half22float2(*reinterpret_cast<const __half2 *>(&u[j]));
-        x[8 * i + 2 * j] = f.x;
-        x[8 * i + 2 * j + 1] = f.y;
-      }
+    for (int i = 0; i < N; i += 2) {
+      const uint32_t u = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(q.data) + at + i);
+      const float2 f = q.dtype == MK_BF16 ? make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u))
+                                          : __half22float2(*reinterpret_cast<const __half2 *>(&u));
+      x[i] = f.x;
+      x[i + 1] = f.y;
     }
   }
 }
@@ -193,35 +228,144 @@ __device__ __forceinline__ void store_out(void *out, int dtype, int64_t at, floa
   else static_cast<__half *>(out)[at] = __float2half_rn(v);
 }
 
+// Four consecutive output elements from a multiple of four.
+__device__ __forceinline__ void store4(void *out, int dtype, int64_t at, float x, float y, float z, float w) {
+  if (dtype == MK_F32) {
+    *reinterpret_cast<float4 *>(static_cast<float *>(out) + at) = make_float4(x, y, z, w);
+  } else if (dtype == MK_BF16) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(x, y), q = __floats2bfloat162_rn(z, w);
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&p), *reinterpret_cast<const uint32_t *>(&q));
+  } else {
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at) = make_uint2(half2_bits(x, y), half2_bits(z, w));
+  }
+}
+
+// o += (scale of a block, brought to the running maximum) x sum over the
+// block's positions of P v, for one chunk.  GT: tiles that share a scale.
+// int8: the digits of P are summed apart, exactly, in 32-bit integers.
+template <int D, int FMT, int MODE, int GT, typename PF, typename WC, typename LIM, typename O>
+__device__ __forceinline__ void add_values(const uint8_t *vs_, const int (&v_at)[2], int pos0, int block,
+                                           const PF &pf, const WC &wc, const LIM &limit, O &o) {
+  constexpr bool INT = FMT == MK_KV8_INT8;
+  constexpr int NO = MODE == kRows16 ? 2 : 1;
+  constexpr int NP = p_terms(FMT, MODE);
+  constexpr int VB = D / 8;
+  // The scale may be NaN (rows that were not finite): it must not reach rows
+  // that see nothing of the block.
+  float by[kTiles / GT][NO][2];
+#pragma unroll
+  for (int b = 0; b < kTiles / GT; ++b) {
+    const float vs = *reinterpret_cast<const float *>(vs_ + kChunk * D + 4 * b * GT);
+    const int begin = (pos0 + 16 * b * GT) & ~(block - 1);
+#pragma unroll
+    for (int j = 0; j < NO; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) by[b][j][c] = begin < limit[j][c] ? vs * wc[j][c] : 0.0f;
+  }
+  uint32_t vw[kTiles][4][VB / 4];
+#pragma unroll
+  for (int tl = 0; tl < kTiles; ++tl)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint8_t *vp = vs_ + v_at[r & 1] + (tl * 16 + (r >> 1) * 8) * D;
+      if constexpr (VB == 16) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(vp);
+        vw[tl][r][0] = u.x; vw[tl][r][1] = u.y; vw[tl][r][2] = u.z; vw[tl][r][3] = u.w;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2 *>(vp);
+        vw[tl][r][0] = u.x; vw[tl][r][1] = u.y;
+      }
+    }
+#pragma unroll
+  for (int w = 0; w < VB / 4; ++w) {  // dims 4 w .. 4 w + 3 of the lane: m-tiles 2 w, 2 w + 1
+    // the four positions 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of a tile: int8, one
+    // word per dim; e4m3, a pair of fp16 for each two
+    uint32_t d[kTiles][INT ? 4 : 8];
+#pragma unroll
+    for (int tl = 0; tl < kTiles; ++tl) {
+      const uint32_t p = __byte_perm(vw[tl][0][w], vw[tl][1][w], 0x5140), q = __byte_perm(vw[tl][0][w], vw[tl][1][w], 0x7362);
+      const uint32_t r = __byte_perm(vw[tl][2][w], vw[tl][3][w], 0x5140), s = __byte_perm(vw[tl][2][w], vw[tl][3][w], 0x7362);
+      if constexpr (INT) {
+        d[tl][0] = __byte_perm(p, r, 0x5410);
+        d[tl][1] = __byte_perm(p, r, 0x7632);
+        d[tl][2] = __byte_perm(q, s, 0x5410);
+        d[tl][3] = __byte_perm(q, s, 0x7632);
+      } else {
+        expand_e4m3(p, d[tl][0], d[tl][1]);
+        expand_e4m3(q, d[tl][2], d[tl][3]);
+        expand_e4m3(r, d[tl][4], d[tl][5]);
+        expand_e4m3(s, d[tl][6], d[tl][7]);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < NO; ++j)
+#pragma unroll
+        for (int b = 0; b < kTiles / GT; ++b) {
+          float v[4];
+          if constexpr (INT) {
+            int acc[NP][4] = {};
+#pragma unroll
+            for (int u = 0; u < NP; ++u) {
+              if constexpr (GT == 2)
+                mma_s8u8(acc[u], d[0][2 * h], d[0][2 * h + 1], d[1][2 * h], d[1][2 * h + 1], pf[j][0][u], pf[j][1][u]);
+              else
+                mma_s8u8(acc[u], d[b][2 * h], d[b][2 * h + 1], pf[j][b][u]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (NP == 2) v[e] = (float)(acc[0][e] * 256 + acc[1][e]);
+              else v[e] = fmaf((float)(acc[0][e] * 256 + acc[1][e]), 256.0f, (float)acc[NP - 1][e]);
+            }
+          } else {
+            v[0] = v[1] = v[2] = v[3] = 0.0f;
+#pragma unroll
+            for (int tl = b * GT; tl < (b + 1) * GT; ++tl)
+#pragma unroll
+              for (int u = 0; u < NP; ++u)
+                mma_f16(v, d[tl][2 * h], d[tl][2 * h + 1], d[tl][4 + 2 * h], d[tl][5 + 2 * h], pf[j][tl][2 * u], pf[j][tl][2 * u + 1]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[j][2 * w + h][e] = fmaf(v[e], by[b][j][e & 1], o[j][2 * w + h][e]);
+        }
+  }
+}
+
 // Chunks [k0, k1) of pair (sequence q.s, kv head hk, row group g) by one CTA;
 // `whole`: they are all of it and the result is final, else it goes to
 // partial slot `slot`.
 template <int D, int FMT, int MODE>
 __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, const SeqRows &q,
                                             int hk, int g, int k0, int k1, bool whole, int slot) {
+  constexpr bool INT = FMT == MK_KV8_INT8;
+  constexpr int W = n_warps(D, MODE);
   constexpr int RG = group_rows(MODE);
-  constexpr int NS = MODE == kRows8 ? 1 : 2;   // column tiles of the scores' MMAs
-  constexpr int NO = MODE == kRows16 ? 2 : 1;  // column tiles of the outputs
-  constexpr int NC = D / 64;                   // 64-dim halves of a row
-  constexpr int VB = D / 8;                    // bytes of a V row that a lane holds
-  constexpr int NM = D / 16;                   // 16-dim m-tiles of the output
-  __shared__ float sh_m[kWarps][RG], sh_l[kWarps][RG];
-  __shared__ int sh_bad;
+  constexpr int NO = MODE == kRows16 ? 2 : 1;            // column tiles of 8 rows
+  constexpr int NQ = q_terms(FMT, MODE), NP = p_terms(FMT, MODE);
+  constexpr int NC = D / 64;                             // 64-dim halves of a row
+  constexpr int NK = INT ? D / 32 : D / 16;              // MMA steps over the dims
+  constexpr int VB = D / 8;                              // bytes of a V row that a lane holds
+  constexpr int NM = D / 16;                             // 16-dim m-tiles of the output
+  __shared__ float sh_m[W][RG], sh_l[W][RG], sh_f[RG];
+  __shared__ int sh_bad, sh_limit[RG];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gq = lane >> 2, t = lane & 3;
   const int P = a.c.page_size, rep = a.rep, n_rows = rep * q.n;
   const int end = q.c + q.n;  // positions of the sequence, its new rows included
   if (threadIdx.x == 0) sh_bad = 0;
 
-  // --- copies: the warp's i-th chunk is chunk k0 + warp + i kWarps ---------
-  uint8_t *ring = smem + warp * kStages * stage_bytes(D);
-  const uint32_t ring_u32 = (uint32_t)__cvta_generic_to_shared(ring);
-  const int n_mine = k1 - k0 > warp ? (k1 - k0 - warp + kWarps - 1) / kWarps : 0;
+  // --- copies: the warp's i-th chunk is chunk k0 + warp + i W ----------------
+  uint8_t *ks_ = smem + warp * 2 * slot_bytes(D), *vs_ = ks_ + slot_bytes(D);
+  const uint32_t ks_u32 = (uint32_t)__cvta_generic_to_shared(ks_);
+  const uint32_t vs_u32 = ks_u32 + slot_bytes(D);
+  const int n_mine = k1 - k0 > warp ? (k1 - k0 - warp + W - 1) / W : 0;
   constexpr int kLook = 32 / kTiles;  // chunks whose pages one lookup (one tile per lane) covers
   const int32_t *table = a.b.d_page_table + (int64_t)q.s * a.b.max_pages;
   bool bad_page = false;
   auto tile_pos = [&](int i0) {  // position of this lane's tile of the lookup at chunk i0
-    return (k0 + warp + (i0 + lane / kTiles) * kWarps) * kChunk + (lane % kTiles) * 16;
+    return (k0 + warp + (i0 + lane / kTiles) * W) * kChunk + (lane % kTiles) * 16;
   };
   auto look = [&](int i0) {
     const int pos = tile_pos(i0);
@@ -239,119 +383,136 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
   };
   int page_next = look(0);
   int64_t rows = 0;
-  auto issue = [&](int i) {
+  // K (or V) codes and scales of chunk i; V follows K, so the lookup is K's.
+  // A warp instruction copies 512 consecutive bytes: four (D = 64: eight) rows.
+  constexpr int kRows = 512 / D;
+  const int my_row = lane / (D / 16);
+  uint32_t to[2];  // where this lane's piece goes, for even and odd groups of rows
+#pragma unroll
+  for (int b = 0; b < 2; ++b) to[b] = slot_at<D>(b * kRows + my_row, (lane % (D / 16)) * 16) - b * 512;
+  auto issue = [&](int i, bool is_v) {
     if (i < n_mine) {
-      if (i % kLook == 0) {
+      if (!is_v && i % kLook == 0) {
         rows = tile_row(i, page_next);
         page_next = look(i + kLook);
       }
-      const uint32_t st = ring_u32 + (i % kStages) * stage_bytes(D);
-      const int pos0 = (k0 + warp + i * kWarps) * kChunk;
+      const int pos0 = (k0 + warp + i * W) * kChunk;
       const int from = (i % kLook) * kTiles;
-      int64_t at[kTiles];
-#pragma unroll
-      for (int tl = 0; tl < kTiles; ++tl) at[tl] = __shfl_sync(0xffffffffu, rows, from + tl);
-      const uint8_t *kp = static_cast<const uint8_t *>(a.c.d_k);
-      const uint8_t *vp = static_cast<const uint8_t *>(a.c.d_v);
+      const uint8_t *src = static_cast<const uint8_t *>(is_v ? a.c.d_v : a.c.d_k) + lane * 16;
+      const uint32_t st = is_v ? vs_u32 : ks_u32;
 #pragma unroll
       for (int tl = 0; tl < kTiles; ++tl) {
-        const int left = end - pos0 - 16 * tl;  // rows of the tile that exist
+        const uint8_t *p = src + __shfl_sync(0xffffffffu, rows, from + tl) * D;
+        const int left = end - pos0 - 16 * tl - my_row;  // rows of the tile that exist, from mine on
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int row = gq + 8 * r;
-            cp_async<16>(st + ((tl * NC + c) * 2 + r) * 512 + lane * 16,
-                         kp + (at[tl] + row) * D + c * 64 + t * 16, row < left);
-          }
+        for (int r = 0; r < 16 / kRows; ++r)
+          cp_async<16>(st + tl * 16 * D + r * 512 + to[r & 1], p + r * 512, r * kRows < left);
       }
-      if (lane < 2 * kTiles) {
-        // lanes 0 .. kTiles-1: K scales, kTiles .. 2 kTiles-1: V scales
-        const int tl = lane % kTiles;
-        const float *sp = lane < kTiles ? a.c.d_k_scale : a.c.d_v_scale;
-        int64_t r = at[0];  // also for a tile past the end: it may share the first one's block
-#pragma unroll
-        for (int j = 1; j < kTiles; ++j) r = tl == j && pos0 + 16 * j < end ? at[j] : r;
-        cp_async<4>(st + 2 * kChunk * D + lane * 4, sp + (r >> a.block_log2), true);
-      }
-      cp_commit();
-#pragma unroll
-      for (int tl = 0; tl < kTiles; ++tl) {
-        const int left = end - pos0 - 16 * tl;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 2 * t + (r & 1) + (r >> 1) * 8;
-          cp_async<VB>(st + kChunk * D + (tl * 4 + r) * (32 * VB) + lane * VB,
-                       vp + (at[tl] + row) * D + gq * VB, row < left);
-        }
-      }
-      cp_commit();
-    } else {
-      cp_commit();
-      cp_commit();
+      // a tile past the end takes the first tile's scale: it may share its block
+      const int tl = lane % kTiles;
+      const int64_t at = __shfl_sync(0xffffffffu, rows, from + (pos0 + 16 * tl < end ? tl : 0));
+      if (lane < kTiles)
+        cp_async<4>(st + kChunk * D + lane * 4,
+                    (is_v ? a.c.d_v_scale : a.c.d_k_scale) + (at >> a.block_log2), true);
     }
+    cp_commit();
   };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  issue(0, false);
+  issue(0, true);
 
-  // --- query rows: column gq of column tile j is row g RG + 8 j + gq --------
-  uint32_t qf[NS][NC * 4][2];
-  float fq[NO];  // f of this lane's row, then of its two columns
-  int lim[NO];
-#pragma unroll
-  for (int j = 0; j < NO; ++j) {
-    const int r = g * RG + 8 * j + gq;
+  // --- query rows, once for all warps: a warp quantises a row at a time ------
+  constexpr int QB = INT ? 1 : 2;  // bytes of a term
+  uint8_t *qs = smem + q_offset(D, MODE);  // [term][row][D]
+  for (int col = warp; col < RG; col += W) {
+    const int r = g * RG + col;
     const bool on = r < n_rows;
     const int i = on ? r / rep : 0;
-    float x[NC][16];
-    float top = 0.0f;
+    float x[D / 32];
+    if (on) {
+      load_row<D / 32>(a.q, (int64_t)(q.r0 + i) * a.q.row_stride + (int64_t)(hk * rep + r - i * rep) * a.q.head_stride + lane * (D / 32), x);
+    } else {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      if (on) {
-        load_q16(a.q, (int64_t)(q.r0 + i) * a.q.row_stride + (int64_t)(hk * rep + r % rep) * a.q.head_stride + c * 64 + t * 16, x[c]);
-      } else {
+      for (int d = 0; d < D / 32; ++d) x[d] = 0.0f;
+    }
+    uint32_t top = 0;  // bits of the largest magnitude: above those of infinity for a NaN
 #pragma unroll
-        for (int d = 0; d < 16; ++d) x[c][d] = 0.0f;
+    for (int d = 0; d < D / 32; ++d) top = max(top, __float_as_uint(x[d]) & 0x7fffffffu);
+    top = __reduce_max_sync(0xffffffffu, top);
+    const int e = (int)(top >> 23) - 126;  // |q| < 2^e
+    const float shrink = ldexpf(1.0f, -e);
+    uint8_t *dst = qs + (col * D + lane * (D / 32)) * QB;
+    constexpr float kOne = INT ? 127.0f * 16384.0f : 1.0f;
+    if constexpr (INT) {
+      // q 2^-e in (-1, 1) times 127 2^14, as a sum of three signed 7-bit digits
+      uint32_t word[NQ] = {};
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) {
+        int n = __float2int_rn(x[d] * shrink * kOne);
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) {
+          const int s = 7 * (NQ - 1 - u);
+          const int digit = s ? (n + (1 << s >> 1)) >> s : n;
+          n -= digit << s;
+          word[u] |= (uint32_t)(digit & 0xff) << (8 * d);
+        }
       }
 #pragma unroll
-      for (int d = 0; d < 16; ++d) top = fmaxf(top, fabsf(x[c][d]));
-    }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int e = (int)(__float_as_uint(top) >> 23) - 126;  // |q| < 2^e
-    const float shrink = ldexpf(1.0f, -e);
-    fq[j] = ldexpf(a.scale * kLog2e, e);
-    lim[j] = on ? q.c + i + 1 : 0;
+      for (int u = 0; u < NQ; ++u) {
+        if constexpr (D == 128) *reinterpret_cast<uint32_t *>(dst + u * RG * D) = word[u];
+        else *reinterpret_cast<uint16_t *>(dst + u * RG * D) = (uint16_t)word[u];
+      }
+    } else {
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const float y0 = x[c][4 * w + 2 * p] * shrink, y1 = x[c][4 * w + 2 * p + 1] * shrink;
-          const uint32_t hi = half2_bits(y0, y1);
-          qf[j][c * 4 + w][p] = hi;
-          if constexpr (MODE == kRows8F32) {
-            // the low term carries a factor 2^11, so that it keeps its bits
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-            qf[1][c * 4 + w][p] = half2_bits((y0 - f.x) * 2048.0f, (y1 - f.y) * 2048.0f);
-          }
+      for (int d = 0; d < D / 32; d += 2) {
+        const float y0 = x[d] * shrink, y1 = x[d + 1] * shrink;
+        const uint32_t hi = half2_bits(y0, y1);
+        *reinterpret_cast<uint32_t *>(dst + 2 * d) = hi;
+        if constexpr (NQ == 2) {
+          // the low term carries a factor 2^11, so that it keeps its bits
+          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+          *reinterpret_cast<uint32_t *>(dst + RG * D * QB + 2 * d) = half2_bits((y0 - f.x) * 2048.0f, (y1 - f.y) * 2048.0f);
         }
+      }
+    }
+    if (lane == 0) {
+      // integers have no NaN: the row's factor carries it
+      sh_f[col] = INT && top >= 0x7f800000u ? __int_as_float(0x7fc00000) : ldexpf(a.scale * kLog2e / kOne, e);
+      sh_limit[col] = on ? q.c + i + 1 : 0;
+    }
   }
-  // columns 2 t, 2 t + 1 of a column tile: what the lanes of rows 2 t, 2 t + 1 hold
-  float f[NO][2];
+  __syncthreads();
+  uint32_t qf[NO][NQ][NK][2];
+  float f[NO][2];  // of the lane's columns 2 t, 2 t + 1 of a column tile
   int limit[NO][2];
-  int least = end;  // positions below it are seen by every row
 #pragma unroll
-  for (int j = 0; j < NO; ++j)
+  for (int j = 0; j < NO; ++j) {
+#pragma unroll
+    for (int u = 0; u < NQ; ++u)
+#pragma unroll
+      for (int c = 0; c < NC * QB; ++c) {
+        // 16 dims (8 for fp16) of row 8 j + gq: INT, half c; else half c / 2
+        const uint4 w = *reinterpret_cast<const uint4 *>(
+            qs + ((u * RG + 8 * j + gq) * D + (c / QB) * 64 + t * 16) * QB + (c % QB) * 16);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) qf[j][u][c * 2 + k / 2][k & 1] = ww[k];
+      }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      f[j][c] = __shfl_sync(0xffffffffu, fq[j], (2 * t + c) * 4);
-      limit[j][c] = __shfl_sync(0xffffffffu, lim[j], (2 * t + c) * 4);
+      f[j][c] = sh_f[8 * j + 2 * t + c];
+      limit[j][c] = sh_limit[8 * j + 2 * t + c];
     }
-  least = q.c + (g * RG) / rep + 1;  // the group's first row sees the fewest
+  }
+  const int least = q.c + (g * RG) / rep + 1;  // the group's first row sees the fewest positions
 
   // --- the warp's chunks ------------------------------------------------------
+  // a lane's pieces: K, 16 bytes of each 64 of the rows gq and gq + 8 of a
+  // tile; V, D / 8 bytes of the rows 2 t, 2 t + 1, 2 t + 8 and 2 t + 9
+  int k_at[NC], v_at[2];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) k_at[c] = slot_at<D>(gq, c * 64 + t * 16);
+#pragma unroll
+  for (int r = 0; r < 2; ++r) v_at[r] = slot_at<D>(2 * t + r, gq * VB);
   float o[NO][NM][4];
   float m[NO][2], l[NO][2];
 #pragma unroll
@@ -364,46 +525,64 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
     l[j][0] = l[j][1] = 0.0f;
   }
   for (int i = 0; i < n_mine; ++i) {
-    __syncwarp();  // the previous chunk's scales have been read
-    issue(i + kStages - 1);
-    const uint8_t *st = ring + (i % kStages) * stage_bytes(D);
-    const int pos0 = (k0 + warp + i * kWarps) * kChunk;
-    cp_wait<2 * kStages - 1>();
+    const int pos0 = (k0 + warp + i * W) * kChunk;
+    cp_wait<1>();  // this chunk's K; its V may still be under way
     __syncwarp();
-    float x[kTiles][NO][4];
-    const float *scales = reinterpret_cast<const float *>(st + 2 * kChunk * D);
+    // scores, in base 2
+    float x[NO][kTiles][4];
 #pragma unroll
     for (int tl = 0; tl < kTiles; ++tl) {
-      float s[NS][4];
-#pragma unroll
-      for (int j = 0; j < NS; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[j][e] = 0.0f;
+          uint32_t w0[NC][4], w1[NC][4];  // rows gq and gq + 8 of the tile
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const uint4 r0 = *reinterpret_cast<const uint4 *>(st + ((tl * NC + c) * 2) * 512 + lane * 16);
-        const uint4 r1 = *reinterpret_cast<const uint4 *>(st + ((tl * NC + c) * 2 + 1) * 512 + lane * 16);
-        const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t a0, a1, a2, a3;
-          expand<FMT>(w0[w], a0, a2);
-          expand<FMT>(w1[w], a1, a3);
-#pragma unroll
-          for (int j = 0; j < NS; ++j)
-            mma_f16(s[j], a0, a1, a2, a3, qf[j][c * 4 + w][0], qf[j][c * 4 + w][1]);
-        }
+        const uint4 r0 = *reinterpret_cast<const uint4 *>(ks_ + k_at[c] + tl * 16 * D);
+        const uint4 r1 = *reinterpret_cast<const uint4 *>(ks_ + k_at[c] + tl * 16 * D + 8 * D);
+        w0[c][0] = r0.x; w0[c][1] = r0.y; w0[c][2] = r0.z; w0[c][3] = r0.w;
+        w1[c][0] = r1.x; w1[c][1] = r1.y; w1[c][2] = r1.z; w1[c][3] = r1.w;
       }
-      const float ks = scales[tl];
+      const float ks = *reinterpret_cast<const float *>(ks_ + kChunk * D + 4 * tl);
+      if constexpr (INT) {
+        int s[NO][NQ][4] = {};
 #pragma unroll
-      for (int j = 0; j < NO; ++j)
+        for (int k = 0; k < NK; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v = s[j][e];
-          if constexpr (MODE == kRows8F32) v = fmaf(s[1][e], 1.0f / 2048.0f, v);
-          x[tl][j][e] = v * (ks * f[j][e & 1]);
+          for (int j = 0; j < NO; ++j)
+#pragma unroll
+            for (int u = 0; u < NQ; ++u)
+              mma_s8(s[j][u], w0[k / 2][2 * (k & 1)], w1[k / 2][2 * (k & 1)], w0[k / 2][2 * (k & 1) + 1],
+                     w1[k / 2][2 * (k & 1) + 1], qf[j][u][k][0], qf[j][u][k][1]);
+#pragma unroll
+        for (int j = 0; j < NO; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v = fmaf((float)s[j][0][e], 16384.0f, (float)(s[j][1][e] * 128 + s[j][NQ - 1][e]));
+            x[j][tl][e] = v * (ks * f[j][e & 1]);
+          }
+      } else {
+        float s[NO][NQ][4] = {};
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          uint32_t a0, a1, a2, a3;
+          expand_e4m3(w0[k / 4][k & 3], a0, a2);
+          expand_e4m3(w1[k / 4][k & 3], a1, a3);
+#pragma unroll
+          for (int j = 0; j < NO; ++j)
+#pragma unroll
+            for (int u = 0; u < NQ; ++u)
+              mma_f16(s[j][u], a0, a1, a2, a3, qf[j][u][k][0], qf[j][u][k][1]);
         }
+#pragma unroll
+        for (int j = 0; j < NO; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v = s[j][0][e];
+            if constexpr (NQ == 2) v = fmaf(s[j][1][e], 1.0f / 2048.0f, v);
+            x[j][tl][e] = v * (ks * f[j][e & 1]);
+          }
+      }
     }
+    __syncwarp();  // every lane has read the scales
+    issue(i + 1, false);
     if (pos0 + kChunk > least) {  // some row does not see all of the chunk
 #pragma unroll
       for (int tl = 0; tl < kTiles; ++tl)
@@ -411,122 +590,82 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
         for (int j = 0; j < NO; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (pos0 + 16 * tl + gq + (e >> 1) * 8 >= limit[j][e & 1]) x[tl][j][e] = -INFINITY;
+            if (pos0 + 16 * tl + gq + (e >> 1) * 8 >= limit[j][e & 1]) x[j][tl][e] = -INFINITY;
     }
-    // a new maximum is rare once a few chunks have passed: all lanes are
-    // asked before any shuffles
-    float mx[NO][2];
-    bool grew = false;
+    // probabilities relative to the chunk's maximum, as B fragments; wc brings
+    // them to the running maximum
+    uint32_t pf[NO][kTiles][INT ? NP : 2 * NP];
+    float wc[NO][2];
 #pragma unroll
-    for (int j = 0; j < NO; ++j)
+    for (int j = 0; j < NO; ++j) {
+      float ref[2], by[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float v = fmaxf(x[0][j][c], x[0][j][c + 2]);
+        float v = fmaxf(x[j][0][c], x[j][0][c + 2]);
 #pragma unroll
-        for (int tl = 1; tl < kTiles; ++tl) v = fmaxf(v, fmaxf(x[tl][j][c], x[tl][j][c + 2]));
-        mx[j][c] = v;
-        grew |= v > m[j][c];
+        for (int tl = 1; tl < kTiles; ++tl) v = fmaxf(v, fmaxf(x[j][tl][c], x[j][tl][c + 2]));
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+        const float now = fmaxf(m[j][c], v);
+        const float base = now == -INFINITY ? 0.0f : now;
+        by[c] = exp2_fast(m[j][c] - base);
+        wc[j][c] = exp2_fast(v - base);
+        ref[c] = v == -INFINITY ? 0.0f : v;
+        m[j][c] = now;
       }
-    if (__any_sync(0xffffffffu, grew)) {
+      float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int j = 0; j < NO; ++j) {
-        float by[2];
+      for (int tl = 0; tl < kTiles; ++tl) {
+        uint32_t r0[2], r1[2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float v = mx[j][c];
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-          v = fmaxf(v, m[j][c]);
-          by[c] = v == -INFINITY ? 1.0f : exp2_fast(m[j][c] - v);
-          m[j][c] = v;
-          l[j][c] *= by[c];
+        for (int r = 0; r < 2; ++r) {
+          constexpr float kUp = p_log2(FMT, MODE);
+          const float p0 = exp2_fast((x[j][tl][2 * r] - ref[0]) + kUp);
+          const float p1 = exp2_fast((x[j][tl][2 * r + 1] - ref[1]) + kUp);
+          sum[0] += p0;
+          sum[1] += p1;
+          if constexpr (INT && NP == 2) {
+            // adding 2^23 rounds to an integer in the low bits
+            r0[r] = transpose8x8(__byte_perm(__float_as_uint(p0 + 8388608.0f),
+                                             __float_as_uint(p1 + 8388608.0f), 0x5410));
+          } else if constexpr (INT) {
+            const uint32_t n0 = __float2uint_rn(p0), n1 = __float2uint_rn(p1);
+            r0[r] = transpose8x8(__byte_perm(n0, n1, 0x6521));
+            r1[r] = transpose8x8(__byte_perm(n0, n1, 0x5410));
+          } else {
+            const uint32_t hi = half2_bits(p0, p1);
+            pf[j][tl][r] = transpose8x8(hi);
+            if constexpr (NP == 2) {
+              const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+              pf[j][tl][2 + r] = transpose8x8(half2_bits(p0 - h.x, p1 - h.y));
+            }
+          }
         }
+        if constexpr (INT) {
+          // bytes of positions 2 t, 2 t + 1, 2 t + 8, 2 t + 9: high, middle, low digit
+          pf[j][tl][0] = __byte_perm(r0[0], r0[1], 0x7531);
+          pf[j][tl][1] = __byte_perm(r0[0], r0[1], 0x6420);
+          if constexpr (NP == 3) pf[j][tl][NP - 1] = __byte_perm(r1[0], r1[1], 0x6420);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) l[j][c] = fmaf(l[j][c], by[c], sum[c] * wc[j][c]);
+      // a new maximum is rare once a few chunks have passed
+      if (__any_sync(0xffffffffu, by[0] != 1.0f || by[1] != 1.0f)) {
 #pragma unroll
         for (int i2 = 0; i2 < NM; ++i2)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[j][i2][e] *= by[e & 1];
       }
     }
-    // probabilities, as the B fragments of the second product
-    uint32_t pf[kTiles][NS][2];
-#pragma unroll
-    for (int j = 0; j < NO; ++j) {
-      float ref[2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) ref[c] = m[j][c] == -INFINITY ? 0.0f : m[j][c] - kPShift;
-#pragma unroll
-      for (int tl = 0; tl < kTiles; ++tl)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float p0 = exp2_fast(x[tl][j][2 * r] - ref[0]), p1 = exp2_fast(x[tl][j][2 * r + 1] - ref[1]);
-          l[j][0] += p0;
-          l[j][1] += p1;
-          const uint32_t hi = half2_bits(p0, p1);
-          pf[tl][j][r] = transpose8x8(hi);
-          if constexpr (MODE == kRows8F32) {
-            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-            pf[tl][1][r] = transpose8x8(half2_bits(p0 - h.x, p1 - h.y));
-          }
-        }
-    }
-    cp_wait<2 * kStages - 2>();
+    cp_wait<1>();  // this chunk's V; the next K may still be under way
     __syncwarp();
-    float part[NO][NM][4];
-#pragma unroll
-    for (int j = 0; j < NO; ++j)
-#pragma unroll
-      for (int i2 = 0; i2 < NM; ++i2)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) part[j][i2][e] = 0.0f;
-#pragma unroll
-    for (int tl = 0; tl < kTiles; ++tl) {
-      uint32_t vw[4][VB / 4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint8_t *vp = st + kChunk * D + (tl * 4 + r) * (32 * VB) + lane * VB;
-        if constexpr (VB == 16) {
-          const uint4 u = *reinterpret_cast<const uint4 *>(vp);
-          vw[r][0] = u.x; vw[r][1] = u.y; vw[r][2] = u.z; vw[r][3] = u.w;
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2 *>(vp);
-          vw[r][0] = u.x; vw[r][1] = u.y;
-        }
-      }
-#pragma unroll
-      for (int w = 0; w < VB / 4; ++w) {
-        uint32_t h0[4], h1[4];  // (positions 2 t, 2 t + 1) and (2 t + 8, 2 t + 9) of four dims
-        expand_pairs<FMT>(vw[0][w], vw[1][w], h0);
-        expand_pairs<FMT>(vw[2][w], vw[3][w], h1);
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int j = 0; j < NO; ++j) {
-            mma_f16(part[j][2 * w + p], h0[2 * p], h0[2 * p + 1], h1[2 * p], h1[2 * p + 1],
-                    pf[tl][j][0], pf[tl][j][1]);
-            if constexpr (MODE == kRows8F32)
-              mma_f16(part[j][2 * w + p], h0[2 * p], h0[2 * p + 1], h1[2 * p], h1[2 * p + 1],
-                      pf[tl][1][0], pf[tl][1][1]);
-          }
-      }
-      const int pos = pos0 + 16 * tl;
-      if (tl == kTiles - 1 || ((pos + 16) & (a.c.block - 1)) == 0) {
-        // the end of the chunk's part of a scale block.  Its scale may be NaN
-        // (not finite rows): it must not reach rows that see nothing of it.
-        const float vs = scales[kTiles + tl];
-        const int begin = pos & ~(a.c.block - 1);
-#pragma unroll
-        for (int j = 0; j < NO; ++j) {
-          const float v[2] = {begin < limit[j][0] ? vs : 0.0f, begin < limit[j][1] ? vs : 0.0f};
-#pragma unroll
-          for (int i2 = 0; i2 < NM; ++i2)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              o[j][i2][e] = fmaf(part[j][i2][e], v[e & 1], o[j][i2][e]);
-              part[j][i2][e] = 0.0f;
-            }
-        }
-      }
-    }
+    if (a.c.block == 16)
+      add_values<D, FMT, MODE, 1>(vs_, v_at, pos0, a.c.block, pf, wc, limit, o);
+    else
+      add_values<D, FMT, MODE, 2>(vs_, v_at, pos0, a.c.block, pf, wc, limit, o);
+    __syncwarp();
+    issue(i + 1, true);
   }
   cp_wait<0>();
 
@@ -537,54 +676,66 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
     for (int c = 0; c < 2; ++c)
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) l[j][c] += __shfl_xor_sync(0xffffffffu, l[j][c], d);
-  __syncthreads();  // every warp is done with its ring: the results go over it
+  __syncthreads();  // every warp is done with its slots: the results go over them
   if (bad_page) sh_bad = 1;
-  const int n_act = min(kWarps, k1 - k0);
   float *om = reinterpret_cast<float *>(smem);
   constexpr int OS = D + 4;  // floats per row: rows begin in different banks
-  if (warp < n_act) {
 #pragma unroll
-    for (int j = 0; j < NO; ++j)
+  for (int j = 0; j < NO; ++j)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = 8 * j + 2 * t + c;
-        if (gq == 0) {
-          sh_m[warp][col] = m[j][c];
-          sh_l[warp][col] = l[j][c];
-        }
-        float *dst = om + (warp * RG + col) * OS + gq * VB;
-#pragma unroll
-        for (int i2 = 0; i2 < NM; ++i2)
-          *reinterpret_cast<float2 *>(dst + 2 * i2) = make_float2(o[j][i2][c], o[j][i2][c + 2]);
+    for (int c = 0; c < 2; ++c) {
+      const int col = 8 * j + 2 * t + c;
+      if (gq == 0) {
+        sh_m[warp][col] = m[j][c];
+        sh_l[warp][col] = l[j][c];
       }
-  }
+      float *dst = om + (warp * RG + col) * OS + gq * VB;
+#pragma unroll
+      for (int i2 = 0; i2 < NM; ++i2)
+        *reinterpret_cast<float2 *>(dst + 2 * i2) = make_float2(o[j][i2][c], o[j][i2][c + 2]);
+    }
   __syncthreads();
-  const bool bad = sh_bad != 0;
-  for (int idx = threadIdx.x; idx < RG * D; idx += kThreads) {
-    const int col = idx / D, d = idx - col * D;
-    const int r = g * RG + col;
-    if (r >= n_rows) continue;
-    float top = -INFINITY;
-    for (int w = 0; w < n_act; ++w) top = fmaxf(top, sh_m[w][col]);
+  if ((int)threadIdx.x < RG) {  // the warps' weights, and the row's maximum and sum
+    const int col = threadIdx.x;
+    float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) top = fmaxf(top, sh_m[w][col]);
     const float ref = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, acc = 0.0f;
-    for (int w = 0; w < n_act; ++w) {
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
       const float by = exp2_fast(sh_m[w][col] - ref);
       sum = fmaf(sh_l[w][col], by, sum);
-      acc = fmaf(om[(w * RG + col) * OS + d], by, acc);
+      sh_m[w][col] = by;
     }
-    if (bad) sum = __int_as_float(0x7fc00000);
+    if (sh_bad) sum = __int_as_float(0x7fc00000);
+    sh_l[0][col] = sum;
+    sh_l[1][col] = top;
+  }
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < RG * (D / 4); idx += W * 32) {
+    const int col = idx / (D / 4), d = (idx - col * (D / 4)) * 4;
+    const int r = g * RG + col;
+    if (r >= n_rows) continue;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float by = sh_m[w][col];
+      const float4 v = *reinterpret_cast<const float4 *>(om + (w * RG + col) * OS + d);
+      acc.x = fmaf(v.x, by, acc.x);
+      acc.y = fmaf(v.y, by, acc.y);
+      acc.z = fmaf(v.z, by, acc.z);
+      acc.w = fmaf(v.w, by, acc.w);
+    }
+    const float sum = sh_l[0][col], top = sh_l[1][col];
     if (whole) {
-      const int i = r / rep, h = hk * rep + r % rep;
-      const int64_t row = (int64_t)(q.r0 + i) * a.n_q_heads + h;
-      store_out(a.out, a.q.dtype, row * D + d, acc / sum);
-      if (a.lse && d == 0) a.lse[row] = (top - kPShift + log2f(sum)) * kLn2;
+      const int i = r / rep;
+      const int64_t row = (int64_t)(q.r0 + i) * a.n_q_heads + hk * rep + r - i * rep;
+      const float by = 1.0f / sum;
+      store4(a.out, a.q.dtype, row * D + d, acc.x * by, acc.y * by, acc.z * by, acc.w * by);
+      if (a.lse && d == 0) a.lse[row] = (top - p_log2(FMT, MODE) + log2f(sum)) * kLn2;
     } else {
-      a.part[((int64_t)slot * RG + col) * D + d] = acc;
-      if (d == 0) {
-        a.ml[((int64_t)slot * RG + col) * 2] = top;
-        a.ml[((int64_t)slot * RG + col) * 2 + 1] = sum;
-      }
+      *reinterpret_cast<float4 *>(a.part + ((int64_t)slot * RG + col) * D + d) = acc;
+      if (d == 0) *reinterpret_cast<float2 *>(a.ml + ((int64_t)slot * RG + col) * 2) = make_float2(top, sum);
     }
   }
   __syncthreads();  // before the next segment's copies and flags
@@ -614,7 +765,7 @@ __device__ __forceinline__ SeqLine seq_line(const AttnArgs &a, const SeqRows &q)
 }
 
 template <int D, int FMT, int MODE>
-__global__ void __launch_bounds__(kThreads, 1) kv8_attention_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(n_warps(D, MODE) * 32, n_ctas(D, MODE)) kv8_attention_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_trigger();  // the merge launch may get ready; it waits for this grid's end
   if (gated(a.gate)) return;
@@ -629,11 +780,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attention_kernel(const __grid
   }
   // The line: every CTA adds up all sequences (thread i takes a run of them)
   // and finds the one in which its piece begins.
-  __shared__ int64_t warp_sum[kWarps];
+  constexpr int W = n_warps(D, MODE);
+  __shared__ int64_t warp_sum[W];
   __shared__ int64_t begin_base;
   __shared__ int begin_seq;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int run = (a.b.n_seqs + kThreads - 1) / kThreads;
+  const int run = (a.b.n_seqs + W * 32 - 1) / (W * 32);
   const int s0 = min(a.b.n_seqs, (int)threadIdx.x * run), s1 = min(a.b.n_seqs, s0 + run);
   int64_t mine = 0;
   for (int s = s0; s < s1; ++s) {
@@ -651,11 +803,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attention_kernel(const __grid
   __syncthreads();
   int64_t total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w < warp) upto += warp_sum[w];
     total += warp_sum[w];
   }
-  const int64_t per = max((int64_t)kMinUnits, (total + gridDim.x - 1) / gridDim.x);
+  const int64_t even = total + gridDim.x - 1;
+  const int64_t per = max((int64_t)kMinUnits, even < (1ll << 32) ? (int64_t)((uint32_t)even / gridDim.x) : even / gridDim.x);
   const int64_t u0 = min(total, per * blockIdx.x), u1 = min(total, u0 + per);
   if (u0 >= upto - mine && u0 < upto) {  // one thread, if the piece is not empty
     int64_t base = upto - mine;
@@ -682,8 +835,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attention_kernel(const __grid
         ++s;
         continue;
       }
-      const int64_t loc = u - base;
-      const int pair = (int)(loc / y.chunks), k0 = (int)(loc - (int64_t)pair * y.chunks);
+      const int loc = (int)(u - base);  // the host allows fewer than 2^31 units of a sequence
+      const int pair = loc / y.chunks, k0 = loc - pair * y.chunks;
       const int k1 = (int)min((int64_t)y.chunks, k0 + (u1 - u));
       const int hk = pair / y.groups, g = pair - hk * y.groups;
       const bool whole = k0 == 0 && k1 == y.chunks;
@@ -692,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attention_kernel(const __grid
       if (k0 == 0 && !whole) {
         // the pair goes on in the CTAs behind this one
         const int64_t last = base + (int64_t)(pair + 1) * y.chunks - 1;
-        cut = make_int4(s, hk, g, (int)(last / per));
+        cut = make_int4(s, hk, g, (int)(last < (1ll << 32) && per < (1ll << 32) ? (uint32_t)last / (uint32_t)per : last / per));
         cut2 = make_int4(q.r0, q.n, 0, 0);
       }
       u += k1 - k0;
@@ -704,35 +857,56 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_attention_kernel(const __grid
   }
 }
 
-// Row blockIdx.y of the cut pair that begins in CTA blockIdx.x of the first
-// launch: its partial results lie in that CTA's slot 2 c + 1 and in the slots
-// 2 c' of the CTAs c' behind it, and are added in that order.
+// The cut pair that begins in CTA blockIdx.x of the first launch, a warp per
+// row: its partial results lie in that CTA's slot 2 c + 1 and in the slots 2 c'
+// of the CTAs c' behind it, and are added in that order.
 template <int D, int RG>
-__global__ void __launch_bounds__(D) kv8_merge_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(RG * 32) kv8_merge_kernel(const __grid_constant__ AttnArgs a, float p_log2) {
   pdl_wait();
   if (gated(a.gate)) return;
-  const int c0 = blockIdx.x;
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31, col = threadIdx.x >> 5;
   const int4 cut = a.head[2 * c0];
   if (cut.x < 0) return;
   const int4 rows = a.head[2 * c0 + 1];
-  const int col = blockIdx.y, r = cut.z * RG + col;
+  const int r = cut.z * RG + col;
   if (r >= a.rep * rows.y) return;
   const int n = cut.w - c0 + 1;
+  const float2 *ml = reinterpret_cast<const float2 *>(a.ml);
   auto slot = [&](int i) { return ((int64_t)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * RG + col); };
   float top = -INFINITY;
-  for (int i = 0; i < n; ++i) top = fmaxf(top, a.ml[slot(i) * 2]);
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, ml[slot(i)].x);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   const float ref = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f, acc = 0.0f;
+  constexpr int N = D / 32;
+  float sum = 0.0f, acc[N] = {};
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const float2 mine = i0 + lane < n ? ml[slot(i0 + lane)] : make_float2(-INFINITY, 0.0f);
+    const float by_mine = exp2_fast(mine.x - ref);
+    const int here = min(32, n - i0);
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float by = exp2_fast(a.ml[slot(i) * 2] - ref);
-    sum = fmaf(a.ml[slot(i) * 2 + 1], by, sum);
-    acc = fmaf(a.part[slot(i) * D + threadIdx.x], by, acc);
+    for (int i = 0; i < here; ++i) {
+      const float by = __shfl_sync(0xffffffffu, by_mine, i);
+      sum = fmaf(__shfl_sync(0xffffffffu, mine.y, i), by, sum);
+      const float *src = a.part + slot(i0 + i) * D + lane * N;
+      if constexpr (N == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(src);
+        acc[0] = fmaf(v.x, by, acc[0]);
+        acc[1] = fmaf(v.y, by, acc[1]);
+        acc[2] = fmaf(v.z, by, acc[2]);
+        acc[3] = fmaf(v.w, by, acc[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2 *>(src);
+        acc[0] = fmaf(v.x, by, acc[0]);
+        acc[1] = fmaf(v.y, by, acc[1]);
+      }
+    }
   }
-  const int i = r / a.rep, h = cut.y * a.rep + r % a.rep;
+  const int i = r / a.rep, h = cut.y * a.rep + r - i * a.rep;
   const int64_t row = (int64_t)(rows.x + i) * a.n_q_heads + h;
-  store_out(a.out, a.q.dtype, row * D + threadIdx.x, acc / sum);
-  if (a.lse && threadIdx.x == 0) a.lse[row] = (top - kPShift + log2f(sum)) * kLn2;
+#pragma unroll
+  for (int d = 0; d < N; ++d) store_out(a.out, a.q.dtype, row * D + lane * N + d, acc[d] / sum);
+  if (a.lse && lane == 0) a.lse[row] = (top - p_log2 + log2f(sum)) * kLn2;
 }
 
 int mode_of(int dtype, int rep, int max_rows) {
@@ -761,14 +935,14 @@ AttnPlan plan_of(const mk_kv8_cache &c, const mk_batch &b, int n_q_heads, int dt
     return p;
   }
   const int sms = sm_count(c.device);
-  p.ctas = (int)std::min<int64_t>(sms, (pairs * chunks + kMinUnits - 1) / kMinUnits);
+  p.ctas = (int)std::min<int64_t>((int64_t)sms * n_ctas(c.head_dim, p.mode), (pairs * chunks + kMinUnits - 1) / kMinUnits);
   p.bytes = (int64_t)p.ctas * (32 + 2 * rg * 8 + 2ll * rg * c.head_dim * 4);
   return p;
 }
 
 template <int D, int FMT, int MODE>
 cudaError_t launch(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
-  constexpr int smem = smem_bytes(D, MODE);
+  constexpr int smem = smem_bytes(D, FMT, MODE);
   static std::atomic<uint64_t> ready{0};  // devices whose limit has been raised
   const uint64_t bit = a.c.device < 64 ? 1ull << a.c.device : 0;
   cudaError_t e = cudaSuccess;
@@ -778,19 +952,19 @@ cudaError_t launch(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  kv8_attention_kernel<D, FMT, MODE><<<p.ctas, kThreads, smem, st>>>(a);
+  kv8_attention_kernel<D, FMT, MODE><<<p.ctas, n_warps(D, MODE) * 32, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.pair_mode) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.ctas, group_rows(MODE));
-  cfg.blockDim = dim3(D);
+  cfg.gridDim = dim3(p.ctas);
+  cfg.blockDim = dim3(group_rows(MODE) * 32);
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<D, group_rows(MODE)>, a);
+  return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<D, group_rows(MODE)>, a, p_log2(FMT, MODE));
 }
 
 template <int D, int FMT>
@@ -807,6 +981,9 @@ const char *check_heads(const mk_kv8_cache *c, int n_q_heads, int dtype, const m
   if (n_q_heads / c->n_kv_heads > 1024) return "more than 1024 query heads per kv head";
   if (dtype < MK_F32 || dtype > MK_F16) return "element type must be MK_F32, MK_BF16 or MK_F16";
   if (b->max_rows > MK_KV8_MAX_ROWS) return "max_rows is above MK_KV8_MAX_ROWS";
+  const int64_t chunks = ((int64_t)b->max_pages * c->page_size + kChunk - 1) / kChunk;
+  if (chunks * c->n_kv_heads * ((int64_t)n_q_heads / c->n_kv_heads * b->max_rows + 7) / 8 >= (1ll << 31))
+    return "page tables of so many positions, with so many heads, are not supported";
   return nullptr;
 }
 

@@ -117,9 +117,16 @@ class Cache:
         H = self.codes[0].shape[2]
         out, lse = np.zeros((R, Hq, D)), np.zeros((R, Hq))
         tol, tol_lse = np.zeros((R, Hq, D)), np.zeros((R, Hq))
-        # one rounding of the probabilities to fp16 (half a step, 2^-11; fp32 rows: two
-        # terms, 2^-21), one of the output to its type
-        t_p = 2.0 ** -21 if dtype == "float32" else 2.0 ** -11
+        # probabilities: e4m3, one rounding to fp16 (half a step, 2^-11; fp32 rows: two terms,
+        # 2^-21); int8, 16-bit integers (fp32 rows: 24-bit, the largest 2^23) relative to the
+        # largest of the 32 positions of their chunk: off by half a unit of that, 2^-16.9 (2^-24)
+        wide = dtype == "float32"
+        t_p = 0.0 if self.fmt == "int8" else 2.0 ** -21 if wide else 2.0 ** -11
+        t_c = 0.0 if self.fmt != "int8" else 2.0 ** -24 if wide else 2.0 ** -16.9
+        # query elements: e4m3, fp16 terms, below 2^-25 of the row's largest rounded away; int8, an
+        # integer of at most 127 2^14 for a row whose largest has at least half of that: half a
+        # unit is at most 2^-21 of the largest
+        t_q = 2.0 ** -21 if self.fmt == "int8" else 2.0 ** -25
         t_o = {"float32": 2.0 ** -24, "bfloat16": 2.0 ** -8, "float16": 2.0 ** -11}[dtype]
         for s, c in enumerate(kv_len):
             n = c + start[s + 1] - start[s]
@@ -139,14 +146,16 @@ class Cache:
                     out[start[s] + i, h] = w @ v[:L, g]
                     lse[start[s] + i, h] = m + math.log(e.sum())
                     # scores: the tensor cores add D / 16 <= 8 partial products and keep at
-                    # least 22 bits of the largest magnitude each time; a query element below
-                    # 2^-25 of its row's largest is rounded away.  That is at most 2^-18 of
-                    # sum |q k|, in the numerator and in the denominator (2^-17).  The sums
-                    # over positions: a warp adds at most L / 128 + 8 products of 16
-                    # positions, each off by 2^-22, and the exponential by 2^-21.
-                    size = (np.abs(k[:L, g]) @ np.abs(x) + np.abs(x).max() * np.abs(k[:L, g]).sum(1) * 2.0 ** -7).max() * abs(scale)
-                    rel = t_p + 2.0 ** -17 * size + 2.0 ** -22 * (L / 64 + 32)
-                    tol[start[s] + i, h] = t_o * np.abs(out[start[s] + i, h]) + 1.01 * rel * (w @ np.abs(v[:L, g])) + 1e-30
+                    # least 22 bits of the largest magnitude each time (int8: exact, then one
+                    # rounding to fp32): at most 2^-18 of sum |q k|, in the numerator and in the
+                    # denominator (2^-17), and so do the elements' own errors.  The sums over
+                    # positions: a warp adds at most L / 128 + 8 products of 16 positions, each
+                    # off by 2^-22, and the exponential by 2^-21.
+                    size = ((np.abs(k[:L, g]) @ np.abs(x)) * 2.0 ** -17 + 2 * t_q * np.abs(x).max() * np.abs(k[:L, g]).sum(1)).max() * abs(scale)
+                    rel = t_p + size + 2.0 ** -22 * (L / 64 + 32)
+                    at = np.arange(0, L, 32)
+                    held = t_c * np.maximum.reduceat(w, at) @ np.add.reduceat(np.abs(v[:L, g]), at)
+                    tol[start[s] + i, h] = t_o * np.abs(out[start[s] + i, h]) + 1.01 * (rel * (w @ np.abs(v[:L, g])) + held) + 1e-30
                     if dtype == "float16":  # smallest steps of the type
                         tol[start[s] + i, h] += 2.0 ** -25
                     tol_lse[start[s] + i, h] = rel + 2.0 ** -23 * (abs(lse[start[s] + i, h]) + 40)
