@@ -448,27 +448,25 @@ class _Status:
 
     def _int32(self, t, n, what):
         """Address of a contiguous int32 tensor of n entries (n None: any) on this device."""
-        if t.dtype is not self._i32 or t.device != self.device or not t.is_contiguous():
+        if t.dtype is not self._i32 or t.get_device() != self._index or not t.is_contiguous():
             _refuse(f"{what} must be a contiguous int32 tensor on {self.device}")
         if n is not None and t.numel() != n:
             _refuse(f"{what} must have {n} entries")
         return t.data_ptr()
 
     def _stream(self, stream):
-        if stream is None:
-            return self._current_stream(self.device).cuda_stream
-        return stream.cuda_stream
+        """The raw stream: the given one, or the device's current one."""
+        return self._raw_stream(self._index) if stream is None else stream.cuda_stream
 
     def _bind(self, device):
         import torch
-        self.device = device
-        self._i32 = torch.int32
-        self._current_stream = torch.cuda.current_stream
-        self._empty = torch.empty
-        self._uint8 = torch.uint8
-        self._lib = lib()
         if device.type != "cuda":
             _refuse(f"tensors must be on a CUDA device, not {device}")
+        self.device, self._index = device, device.index
+        self._i32, self._uint8, self._f32 = torch.int32, torch.uint8, torch.float32
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._empty = torch.empty
+        self._lib = lib()
 
 
 class KV8Cache(_Status):
@@ -509,10 +507,15 @@ class KV8Cache(_Status):
                            k_scale.data_ptr(), v_scale.data_ptr(), self.status.data_ptr())
         self._dtypes = {torch.float32: MK_F32, torch.bfloat16: MK_BF16, torch.float16: MK_F16}
         self._workspaces = {}
-        self._ref = ctypes.byref(self._c)
-        _check(self._lib.mk_kv8_attention_workspace(self._ref, n_kv_heads, MK_BF16, ctypes.byref(
-            Batch(1, 1, 1, 1, None, self.status.data_ptr(), self.status.data_ptr())),
-            ctypes.byref(ctypes.c_int64())))  # the library's own checks of the cache
+        # the argument structures of a call, refilled by every call
+        self._ref = ctypes.addressof(self._c)
+        self._args = tuple(x() for x in (Rows, Rows, Batch))
+        self._at = tuple(ctypes.addressof(x) for x in self._args)
+        self._batch_args = self._args[2]
+        # the library's own checks of the cache
+        self._fill_batch(None, 1, 1, 1, 1, self.status.data_ptr(), self.status.data_ptr())
+        _check(self._lib.mk_kv8_attention_workspace(self._ref, n_kv_heads, MK_BF16, self._at[2],
+                                                    ctypes.byref(ctypes.c_int64())))
 
     @classmethod
     def empty(cls, n_pages, n_layers, n_kv_heads, head_dim, page_size=64, block=64, dtype=None,
@@ -531,37 +534,53 @@ class KV8Cache(_Status):
         """The tensors whose first dimension are pages, for PagePool."""
         return [self.k, self.v, self.k_scale, self.v_scale]
 
-    def _rows(self, x, n_heads, what):
-        if x.dim() != 3 or (n_heads and x.shape[1] != n_heads) or x.shape[2] != self.head_dim \
-                or x.stride(2) != 1:
+    def _rows(self, slot, x, n_heads, what):
+        """Fills argument structure `slot` with the rows x; returns their number."""
+        shape, stride = x.shape, x.stride()
+        if len(shape) != 3 or (n_heads and shape[1] != n_heads) or shape[2] != self.head_dim \
+                or stride[2] != 1:
             _refuse(f"{what} must be [rows][{n_heads or 'heads'}][{self.head_dim}] with contiguous "
                     "head_dim")
-        if x.dtype not in self._dtypes or x.device != self.device:
+        dtype = self._dtypes.get(x.dtype)
+        if dtype is None or x.get_device() != self._index:
             _refuse(f"{what} must be float32, bfloat16 or float16 on {self.device}")
-        return Rows(x.data_ptr(), self._dtypes[x.dtype], x.stride(0), x.stride(1))
+        r = self._args[slot]
+        r.data, r.dtype, r.row_stride, r.head_stride = x.data_ptr(), dtype, stride[0], stride[1]
+        return shape[0]
+
+    def _fill_batch(self, start, n_seqs, n_rows, max_rows, max_pages, kv_len, page_table):
+        b = self._batch_args
+        b.n_seqs, b.n_rows, b.max_rows, b.max_pages = n_seqs, n_rows, max_rows, max_pages
+        b.d_row_start, b.d_kv_len, b.d_page_table = start, kv_len, page_table
 
     def _batch(self, page_table, kv_len, row_start, n_rows, max_rows):
-        if page_table.dim() != 2 or page_table.shape[1] < 1:
+        shape = page_table.shape
+        if len(shape) != 2 or shape[1] < 1:
             _refuse("page_table must be [n_seqs][max_pages]")
-        n, max_pages = page_table.shape
-        start = None if row_start is None else self._int32(row_start, n + 1, "row_start")
-        if row_start is None and n_rows != n:
-            _refuse("without row_start there is one row per sequence")
-        return Batch(n, n_rows, max_rows, max_pages, start, self._int32(kv_len, n, "kv_len"),
-                     self._int32(page_table, None, "page_table"))
+        n, max_pages = shape
+        if row_start is None:
+            if n_rows != n:
+                _refuse("without row_start there is one row per sequence")
+            start = None
+        else:
+            start = self._int32(row_start, n + 1, "row_start")
+        self._fill_batch(start, n, n_rows, max_rows, max_pages, self._int32(kv_len, n, "kv_len"),
+                         self._int32(page_table, None, "page_table"))
+        return n, max_pages
 
     def store(self, layer, k, v, page_table, kv_len, row_start=None, stream=None):
         """mk_kv8_store: quantise the new rows k, v [n_rows][n_kv_heads][head_dim] (float32,
         bfloat16 or float16) and append them to layer `layer`; rows row_start[s] to
         row_start[s + 1] - 1 (row s without row_start) go to the positions from kv_len[s]."""
-        n_rows = k.shape[0]
-        if v.shape != k.shape or v.dtype != k.dtype:
+        n_rows = self._rows(0, k, self.n_kv_heads, "k")
+        if self._rows(1, v, self.n_kv_heads, "v") != n_rows or v.dtype is not k.dtype:
             _refuse("k and v differ in shape or type")
-        rk, rv = self._rows(k, self.n_kv_heads, "k"), self._rows(v, self.n_kv_heads, "v")
-        b = self._batch(page_table, kv_len, row_start, n_rows, max(1, n_rows))
+        self._batch(page_table, kv_len, row_start, n_rows, n_rows or 1)
         if n_rows:
-            _check(self._lib.mk_kv8_store(self._ref, layer, ctypes.byref(rk), ctypes.byref(rv),
-                                          ctypes.byref(b), self._stream(stream)))
+            rk, rv, b = self._at
+            rc = self._lib.mk_kv8_store(self._ref, layer, rk, rv, b, self._stream(stream))
+            if rc:
+                _check(rc)
 
     def attention(self, layer, q, page_table, kv_len, row_start=None, max_rows=None, scale=None,
                   out=None, return_lse=False, stream=None):
@@ -569,36 +588,39 @@ class KV8Cache(_Status):
         positions 0 to kv_len[s] + i.  max_rows bounds the rows of one sequence (1 without
         row_start; at most MK_KV8_MAX_ROWS).  Returns the output in q's type, and with
         return_lse also the float32 log-sum-exp [n_rows][n_q_heads]."""
-        n_rows, n_heads = q.shape[0], q.shape[1] if q.dim() == 3 else 0
-        rq = self._rows(q, 0, "q")
+        n_rows = self._rows(0, q, 0, "q")
+        n_heads = q.shape[1]
         if max_rows is None:
             if row_start is not None:
                 _refuse("max_rows is needed with row_start")
             max_rows = 1
-        b = self._batch(page_table, kv_len, row_start, n_rows, max_rows)
+        n, max_pages = self._batch(page_table, kv_len, row_start, n_rows, max_rows)
         if out is None:
             out = self._empty((n_rows, n_heads, self.head_dim), dtype=q.dtype, device=self.device)
         elif out.shape != q.shape or out.dtype != q.dtype or out.device != self.device \
                 or not out.is_contiguous():
             _refuse("out must be contiguous, with the shape, type and device of q")
-        lse = self._empty((n_rows, n_heads), dtype=self.k_scale.dtype, device=self.device) \
+        lse = self._empty((n_rows, n_heads), dtype=self._f32, device=self.device) \
             if return_lse else None
-        if scale is None:
-            scale = self.head_dim ** -0.5
-        key = (n_heads, rq.dtype, b.n_seqs, max_rows, b.max_pages)
+        rq, _, b = self._at
+        # the workspace's size follows from the sizes alone
+        key = (n_heads, q.dtype, n, max_rows, max_pages)
         size = self._workspaces.get(key)
         if size is None:
             bytes_ = ctypes.c_int64()
-            _check(self._lib.mk_kv8_attention_workspace(self._ref, n_heads, rq.dtype,
-                                                        ctypes.byref(b), ctypes.byref(bytes_)))
+            _check(self._lib.mk_kv8_attention_workspace(self._ref, n_heads, self._args[0].dtype, b,
+                                                        ctypes.byref(bytes_)))
             size = self._workspaces[key] = bytes_.value
         if n_rows:
             # a workspace of its own for every call: calls on other streams and
             # captured graphs do not meet in it
             ws = self._empty(size, dtype=self._uint8, device=self.device) if size else None
-            _check(self._lib.mk_kv8_attention(
-                self._ref, layer, ctypes.byref(rq), n_heads, scale, out.data_ptr(), _ptr(lse),
-                ctypes.byref(b), _ptr(ws), size, self._stream(stream)))
+            rc = self._lib.mk_kv8_attention(
+                self._ref, layer, rq, n_heads, self.head_dim ** -0.5 if scale is None else scale,
+                out.data_ptr(), lse.data_ptr() if return_lse else None, b,
+                ws.data_ptr() if size else None, size, self._stream(stream))
+            if rc:
+                _check(rc)
             if ws is not None and stream is not None:
                 ws.record_stream(stream)
         return (out, lse) if return_lse else out
@@ -633,7 +655,7 @@ class PagePool(_Status):
         p.d_page_table = self._int32(page_table, None, "page_table")
         p.d_ref = self._int32(ref_count, None, "ref_count")
         p.d_status = self.status.data_ptr()
-        self._ref = ctypes.byref(p)
+        self._ref = ctypes.addressof(p)
         self._sizes = {}
         self._workspace(0)
 
@@ -657,7 +679,9 @@ class PagePool(_Status):
     def _call(self, fn, n, args, stream):
         size = self._workspace(n)
         ws = self._empty(size, dtype=self._uint8, device=self.device)
-        _check(fn(self._ref, *args, ws.data_ptr(), size, self._stream(stream)))
+        rc = fn(self._ref, *args, ws.data_ptr(), size, self._stream(stream))
+        if rc:
+            _check(rc)
         if stream is not None:
             ws.record_stream(stream)
 
