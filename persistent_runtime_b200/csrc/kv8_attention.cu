@@ -59,7 +59,7 @@ namespace {
 constexpr int kChunk = 32;            // positions of a warp's step
 constexpr int kTiles = kChunk / 16;   // 16-position MMA tiles of a chunk
 constexpr int kPairChunks = 16;       // longest pair (in chunks) that one CTA takes whole
-constexpr int kMinUnits = 4;          // shortest piece (in chunks) of the cut line
+constexpr int kMinUnits = 4;          // shortest piece of the cut line, in units (chunks)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // How the query rows fill the MMA columns: 8 rows of a 16-bit type, 16 rows of
@@ -67,13 +67,37 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // one of low terms).
 enum Mode { kRows8 = 0, kRows16 = 1, kRows8F32 = 2 };
 
+// Division of numbers below 2^31 by a divisor that the host knows: with 2^s the
+// first power of two >= d and mul = ceil(2^(31 + s) / d), n mul / 2^(31 + s)
+// exceeds n / d by less than n / 2^(31 + s) < 1 / d.
+struct Divisor {
+  uint32_t mul;
+  int shift, d;
+  Divisor() = default;
+  explicit Divisor(int by) : shift(0), d(by) {
+    while ((1ll << shift) < by) ++shift;
+    mul = (uint32_t)(((1ull << (31 + shift)) + by - 1) / by);
+  }
+  __device__ __forceinline__ int quotient(int n) const {
+    return (int)(((uint64_t)(uint32_t)n * mul) >> (31 + shift));
+  }
+};
+// n / d for a quotient below 2^21: the estimate is off by one at most.
+__device__ __forceinline__ int small_quotient(int n, int d) {
+  int q = (int)__fdividef((float)n, (float)d);
+  const int r = n - q * d;
+  q += r >= d ? 1 : r < 0 ? -1 : 0;
+  return q;
+}
+
 struct AttnArgs {
   mk_kv8_cache c;
   mk_batch b;
   mk_rows q;
   void *out;
   float *lse;
-  int layer, n_q_heads, rep;
+  int layer, n_q_heads;
+  Divisor by_page, by_rep, by_grid;
   float scale;
   int block_log2;
   int pair_mode;  // a CTA takes the pair blockIdx.x, nothing is cut
@@ -89,6 +113,10 @@ constexpr int group_rows(int mode) { return mode == kRows16 ? 16 : 8; }
 // Warps of a CTA and CTAs per SM: as many as their registers allow.
 __host__ __device__ constexpr int n_warps(int, int mode) { return mode == kRows8F32 ? 4 : 8; }
 __host__ __device__ constexpr int n_ctas(int, int mode) { return mode == kRows8F32 ? 2 : 1; }
+
+// What a pair costs a CTA besides its chunks (query rows, the warps' results),
+// in units of a chunk.
+__host__ __device__ constexpr int pair_units(int mode) { return mode == kRows16 ? 16 : 8; }
 
 // Terms of a query element in the MMAs (int8: three signed 7-bit digits, fp16:
 // one or, for fp32 rows, two numbers) and of a probability (8-bit digits; fp16
@@ -228,17 +256,27 @@ __device__ __forceinline__ void store_out(void *out, int dtype, int64_t at, floa
   else static_cast<__half *>(out)[at] = __float2half_rn(v);
 }
 
-// Four consecutive output elements from a multiple of four.
-__device__ __forceinline__ void store4(void *out, int dtype, int64_t at, float x, float y, float z, float w) {
+// The dim in place 16 i + 2 g (+ 1) of a row of results is D / 8 g + 2 i (+ 1).
+template <int D>
+__device__ __forceinline__ int dim_of(int place) {
+  return ((place & 15) >> 1) * (D / 8) + (place >> 4) * 2 + (place & 1);
+}
+// Two output elements at an even place.
+__device__ __forceinline__ void store2(void *out, int dtype, int64_t at, float x, float y) {
   if (dtype == MK_F32) {
-    *reinterpret_cast<float4 *>(static_cast<float *>(out) + at) = make_float4(x, y, z, w);
+    *reinterpret_cast<float2 *>(static_cast<float *>(out) + at) = make_float2(x, y);
   } else if (dtype == MK_BF16) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(x, y), q = __floats2bfloat162_rn(z, w);
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&p), *reinterpret_cast<const uint32_t *>(&q));
+    const __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
+    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(out) + at) = *reinterpret_cast<const uint32_t *>(&p);
   } else {
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at) = make_uint2(half2_bits(x, y), half2_bits(z, w));
+    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(out) + at) = half2_bits(x, y);
   }
+}
+// Places p .. p + 3 (p a multiple of 4) of the row of results at element `row`.
+template <int D>
+__device__ __forceinline__ void store_places(void *out, int dtype, int64_t row, int p, float x, float y, float z, float w) {
+  store2(out, dtype, row + dim_of<D>(p), x, y);
+  store2(out, dtype, row + dim_of<D>(p + 2), z, w);
 }
 
 // o += (scale of a block, brought to the running maximum) x sum over the
@@ -352,7 +390,7 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
   __shared__ int sh_bad, sh_limit[RG];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gq = lane >> 2, t = lane & 3;
-  const int P = a.c.page_size, rep = a.rep, n_rows = rep * q.n;
+  const int P = a.c.page_size, rep = a.by_rep.d, n_rows = rep * q.n;
   const int end = q.c + q.n;  // positions of the sequence, its new rows included
   if (threadIdx.x == 0) sh_bad = 0;
 
@@ -369,7 +407,7 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
   };
   auto look = [&](int i0) {
     const int pos = tile_pos(i0);
-    return i0 + lane / kTiles < n_mine && pos < end ? table[pos / P] : 0;
+    return i0 + lane / kTiles < n_mine && pos < end ? table[a.by_page.quotient(pos)] : 0;
   };
   auto tile_row = [&](int i0, int page) -> int64_t {  // row of the pool where the tile begins
     const int pos = tile_pos(i0);
@@ -379,7 +417,7 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
       record_status(a.c.d_status, MK_ERR_DEVICE, q.s, page, MK_CHECK_PAGE);
       return 0;
     }
-    return kv8_slab(a.c, a.layer, page, hk) * P + pos % P;
+    return kv8_slab(a.c, a.layer, page, hk) * P + (pos - a.by_page.quotient(pos) * P);
   };
   int page_next = look(0);
   int64_t rows = 0;
@@ -417,23 +455,31 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
     }
     cp_commit();
   };
-  issue(0, false);
-  issue(0, true);
-
   // --- query rows, once for all warps: a warp quantises a row at a time ------
   constexpr int QB = INT ? 1 : 2;  // bytes of a term
+  constexpr int NR = (RG + W - 1) / W;
   uint8_t *qs = smem + q_offset(D, MODE);  // [term][row][D]
-  for (int col = warp; col < RG; col += W) {
-    const int r = g * RG + col;
-    const bool on = r < n_rows;
-    const int i = on ? r / rep : 0;
-    float x[D / 32];
-    if (on) {
-      load_row<D / 32>(a.q, (int64_t)(q.r0 + i) * a.q.row_stride + (int64_t)(hk * rep + r - i * rep) * a.q.head_stride + lane * (D / 32), x);
+  float x_row[NR][D / 32];
+  int lim_row[NR];
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    const int col = warp + n * W, r = g * RG + col;
+    const int i = a.by_rep.quotient(r);
+    lim_row[n] = col < RG && r < n_rows ? q.c + i + 1 : 0;
+    if (lim_row[n]) {
+      load_row<D / 32>(a.q, (int64_t)(q.r0 + i) * a.q.row_stride + (int64_t)(hk * rep + r - i * rep) * a.q.head_stride + lane * (D / 32), x_row[n]);
     } else {
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d) x[d] = 0.0f;
+      for (int d = 0; d < D / 32; ++d) x_row[n][d] = 0.0f;
     }
+  }
+  issue(0, false);
+  issue(0, true);
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    const int col = warp + n * W;
+    if (RG % W != 0 && col >= RG) break;
+    const float(&x)[D / 32] = x_row[n];
     uint32_t top = 0;  // bits of the largest magnitude: above those of infinity for a NaN
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) top = max(top, __float_as_uint(x[d]) & 0x7fffffffu);
@@ -477,7 +523,7 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
     if (lane == 0) {
       // integers have no NaN: the row's factor carries it
       sh_f[col] = INT && top >= 0x7f800000u ? __int_as_float(0x7fc00000) : ldexpf(a.scale * kLog2e / kOne, e);
-      sh_limit[col] = on ? q.c + i + 1 : 0;
+      sh_limit[col] = lim_row[n];
     }
   }
   __syncthreads();
@@ -503,7 +549,7 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
       limit[j][c] = sh_limit[8 * j + 2 * t + c];
     }
   }
-  const int least = q.c + (g * RG) / rep + 1;  // the group's first row sees the fewest positions
+  const int least = q.c + a.by_rep.quotient(g * RG) + 1;  // the group's first row sees the fewest positions
 
   // --- the warp's chunks ------------------------------------------------------
   // a lane's pieces: K, 16 bytes of each 64 of the rows gq and gq + 8 of a
@@ -689,10 +735,12 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
         sh_m[warp][col] = m[j][c];
         sh_l[warp][col] = l[j][c];
       }
-      float *dst = om + (warp * RG + col) * OS + gq * VB;
+      // dims gq VB + 2 i2, + 1 go to place 16 i2 + 2 gq: neighbouring lanes write
+      // neighbouring places
+      float *dst = om + (warp * RG + col) * OS + 2 * gq;
 #pragma unroll
       for (int i2 = 0; i2 < NM; ++i2)
-        *reinterpret_cast<float2 *>(dst + 2 * i2) = make_float2(o[j][i2][c], o[j][i2][c + 2]);
+        *reinterpret_cast<float2 *>(dst + 16 * i2) = make_float2(o[j][i2][c], o[j][i2][c + 2]);
     }
   __syncthreads();
   if ((int)threadIdx.x < RG) {  // the warps' weights, and the row's maximum and sum
@@ -728,10 +776,10 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
     }
     const float sum = sh_l[0][col], top = sh_l[1][col];
     if (whole) {
-      const int i = r / rep;
+      const int i = a.by_rep.quotient(r);
       const int64_t row = (int64_t)(q.r0 + i) * a.n_q_heads + hk * rep + r - i * rep;
       const float by = 1.0f / sum;
-      store4(a.out, a.q.dtype, row * D + d, acc.x * by, acc.y * by, acc.z * by, acc.w * by);
+      store_places<D>(a.out, a.q.dtype, row * D, d, acc.x * by, acc.y * by, acc.z * by, acc.w * by);
       if (a.lse && d == 0) a.lse[row] = (top - p_log2(FMT, MODE) + log2f(sum)) * kLn2;
     } else {
       *reinterpret_cast<float4 *>(a.part + ((int64_t)slot * RG + col) * D + d) = acc;
@@ -751,23 +799,24 @@ __device__ __noinline__ void reject(const AttnArgs &a, const SeqRows &q) {
     for (int64_t i = 0; i < n; ++i) a.lse[r0 + i] = nan;
 }
 
-// Chunks on the line of sequence s: pairs x chunks of one pair.
+// Units on the line of sequence s: for every pair its chunks, then
+// pair_units that stand for what it costs besides.
 struct SeqLine {
-  int chunks, groups;
-  int64_t units;
+  int chunks, groups, units;
 };
 template <int MODE>
 __device__ __forceinline__ SeqLine seq_line(const AttnArgs &a, const SeqRows &q) {
   if (q.bad || q.n == 0) return {0, 0, 0};
-  const int chunks = (int)(((int64_t)q.c + q.n + kChunk - 1) / kChunk);
-  const int groups = (a.rep * q.n + group_rows(MODE) - 1) / group_rows(MODE);
-  return {chunks, groups, (int64_t)chunks * groups * a.c.n_kv_heads};
+  const int chunks = (q.c + q.n + kChunk - 1) / kChunk;
+  const int groups = (a.by_rep.d * q.n + group_rows(MODE) - 1) / group_rows(MODE);
+  return {chunks, groups, (chunks + pair_units(MODE)) * groups * a.c.n_kv_heads};
 }
 
 template <int D, int FMT, int MODE>
 __global__ void __launch_bounds__(n_warps(D, MODE) * 32, n_ctas(D, MODE)) kv8_attention_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  pdl_trigger();  // the merge launch may get ready; it waits for this grid's end
+  pdl_trigger();  // the launch behind this one may get ready; it waits for this grid's end
+  pdl_wait();
   if (gated(a.gate)) return;
   if (a.pair_mode) {
     const int g = blockIdx.x % a.groups, rest = blockIdx.x / a.groups;
@@ -778,78 +827,75 @@ __global__ void __launch_bounds__(n_warps(D, MODE) * 32, n_ctas(D, MODE)) kv8_at
     if (g < y.groups) run_segment<D, FMT, MODE>(a, smem, q, hk, g, 0, y.chunks, true, 0);
     return;
   }
-  // The line: every CTA adds up all sequences (thread i takes a run of them)
-  // and finds the one in which its piece begins.
-  constexpr int W = n_warps(D, MODE);
-  __shared__ int64_t warp_sum[W];
-  __shared__ int64_t begin_base;
-  __shared__ int begin_seq;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int run = (a.b.n_seqs + W * 32 - 1) / (W * 32);
-  const int s0 = min(a.b.n_seqs, (int)threadIdx.x * run), s1 = min(a.b.n_seqs, s0 + run);
-  int64_t mine = 0;
-  for (int s = s0; s < s1; ++s) {
-    const SeqRows q = seq_rows(a.b, a.c.page_size, s);
-    if (q.bad && s % (int)gridDim.x == (int)blockIdx.x) reject(a, q);
-    mine += seq_line<MODE>(a, q).units;
-  }
-  int64_t upto = mine;
+  // The line: every warp adds up all sequences, 32 at a time, and finds the one
+  // in which the CTA's piece begins.
+  const int lane = threadIdx.x & 31;
+  SeqRows mine;   // sequence s0 + lane
+  SeqLine line;
+  int upto;       // units of the sequences s0 .. s0 + lane
+  int s0;
+  auto group = [&](int first) {
+    s0 = first;
+    line = SeqLine{0, 0, 0};
+    mine = SeqRows{first + lane, 0, 0, 0, 0};
+    if (first + lane < a.b.n_seqs) {
+      mine = seq_rows(a.b, a.c.page_size, first + lane);
+      line = seq_line<MODE>(a, mine);
+    }
+    upto = line.units;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
-    if (lane >= d) upto += v;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += v;
+    }
+  };
+  int total = 0;
+  for (int first = 0; first < a.b.n_seqs; first += 32) {
+    group(first);
+    if (mine.bad && threadIdx.x < 32 && mine.s % (int)gridDim.x == (int)blockIdx.x) reject(a, mine);
+    total += __shfl_sync(0xffffffffu, upto, 31);
   }
-  if (lane == 31) warp_sum[warp] = upto;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    if (w < warp) upto += warp_sum[w];
-    total += warp_sum[w];
-  }
-  const int64_t even = total + gridDim.x - 1;
-  const int64_t per = max((int64_t)kMinUnits, even < (1ll << 32) ? (int64_t)((uint32_t)even / gridDim.x) : even / gridDim.x);
-  const int64_t u0 = min(total, per * blockIdx.x), u1 = min(total, u0 + per);
-  if (u0 >= upto - mine && u0 < upto) {  // one thread, if the piece is not empty
-    int64_t base = upto - mine;
-    for (int s = s0; s < s1; ++s) {
-      const int64_t n = seq_line<MODE>(a, seq_rows(a.b, a.c.page_size, s)).units;
-      if (u0 < base + n) {
-        begin_seq = s;
-        begin_base = base;
-        break;
-      }
-      base += n;
+  // the host allows fewer than 2^30 units
+  const int per = max(kMinUnits, a.by_grid.quotient(total + (int)gridDim.x - 1));
+  const int u0 = (int)min((int64_t)total, (int64_t)per * blockIdx.x), u1 = min(total, u0 + per);
+  int base0 = 0;  // units before sequence s0
+  if (a.b.n_seqs > 32 && u0 < u1) {
+    group(0);
+    while (u0 >= base0 + __shfl_sync(0xffffffffu, upto, 31)) {
+      base0 += __shfl_sync(0xffffffffu, upto, 31);
+      group(s0 + 32);
     }
   }
-  __syncthreads();
   int4 cut = make_int4(-1, 0, 0, 0), cut2 = make_int4(0, 0, 0, 0);
-  if (u0 < u1) {
-    int s = begin_seq;
-    int64_t base = begin_base, u = u0;
-    while (u < u1) {
-      const SeqRows q = seq_rows(a.b, a.c.page_size, s);
-      const SeqLine y = seq_line<MODE>(a, q);
-      if (u >= base + y.units) {
-        base += y.units;
-        ++s;
-        continue;
-      }
-      const int loc = (int)(u - base);  // the host allows fewer than 2^31 units of a sequence
-      const int pair = loc / y.chunks, k0 = loc - pair * y.chunks;
-      const int k1 = (int)min((int64_t)y.chunks, k0 + (u1 - u));
-      const int hk = pair / y.groups, g = pair - hk * y.groups;
-      const bool whole = k0 == 0 && k1 == y.chunks;
-      run_segment<D, FMT, MODE>(a, smem, q, hk, g, k0, k1, whole,
-                                2 * (int)blockIdx.x + (k0 == 0 ? 1 : 0));
+  int u = u0;
+  while (u < u1) {
+    // the sequence of unit u: the first lane whose sequences reach beyond it
+    const uint32_t beyond = __ballot_sync(0xffffffffu, base0 + upto > u);
+    if (beyond == 0) {
+      base0 += __shfl_sync(0xffffffffu, upto, 31);
+      group(s0 + 32);
+      continue;
+    }
+    const int at = __ffs(beyond) - 1;
+    const SeqRows q{s0 + at, __shfl_sync(0xffffffffu, mine.r0, at), __shfl_sync(0xffffffffu, mine.n, at),
+                    __shfl_sync(0xffffffffu, mine.c, at), 0};
+    const int chunks = __shfl_sync(0xffffffffu, line.chunks, at);
+    const int groups = __shfl_sync(0xffffffffu, line.groups, at);
+    const int base = base0 + __shfl_sync(0xffffffffu, upto - line.units, at);
+    const int len = chunks + pair_units(MODE);
+    const int pair = small_quotient(u - base, len), k0 = u - base - pair * len;
+    const int k1 = min(chunks, k0 + u1 - u);
+    if (k0 < chunks) {
+      const int hk = groups == 1 ? pair : small_quotient(pair, groups), g = pair - hk * groups;
+      const bool whole = k0 == 0 && k1 == chunks;
+      run_segment<D, FMT, MODE>(a, smem, q, hk, g, k0, k1, whole, 2 * (int)blockIdx.x + (k0 == 0 ? 1 : 0));
       if (k0 == 0 && !whole) {
-        // the pair goes on in the CTAs behind this one
-        const int64_t last = base + (int64_t)(pair + 1) * y.chunks - 1;
-        cut = make_int4(s, hk, g, (int)(last < (1ll << 32) && per < (1ll << 32) ? (uint32_t)last / (uint32_t)per : last / per));
+        // the pair goes on in the CTAs behind this one, to that of its last chunk
+        cut = make_int4(q.s, hk, g, small_quotient(base + pair * len + chunks - 1, per));
         cut2 = make_int4(q.r0, q.n, 0, 0);
       }
-      u += k1 - k0;
     }
+    u = base + (pair + 1) * len;  // the next pair, if the piece goes that far
   }
   if (threadIdx.x == 0) {
     a.head[2 * blockIdx.x] = cut;
@@ -862,50 +908,70 @@ __global__ void __launch_bounds__(n_warps(D, MODE) * 32, n_ctas(D, MODE)) kv8_at
 // of the CTAs c' behind it, and are added in that order.
 template <int D, int RG>
 __global__ void __launch_bounds__(RG * 32) kv8_merge_kernel(const __grid_constant__ AttnArgs a, float p_log2) {
+  pdl_trigger();
   pdl_wait();
   if (gated(a.gate)) return;
   const int c0 = blockIdx.x, lane = threadIdx.x & 31, col = threadIdx.x >> 5;
-  const int4 cut = a.head[2 * c0];
-  if (cut.x < 0) return;
-  const int4 rows = a.head[2 * c0 + 1];
-  const int r = cut.z * RG + col;
-  if (r >= a.rep * rows.y) return;
-  const int n = cut.w - c0 + 1;
+  // what most pairs need is loaded before it is known how many CTAs took part
+  constexpr int N = D / 32;
   const float2 *ml = reinterpret_cast<const float2 *>(a.ml);
   auto slot = [&](int i) { return ((int64_t)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * RG + col); };
-  float top = -INFINITY;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, ml[slot(i)].x);
+  auto load = [&](int i, float (&v)[N]) {
+    const float *src = a.part + slot(i) * D + lane * N;
+    if constexpr (N == 4) {
+      const float4 u = *reinterpret_cast<const float4 *>(src);
+      v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+    } else {
+      const float2 u = *reinterpret_cast<const float2 *>(src);
+      v[0] = u.x; v[1] = u.y;
+    }
+  };
+  const int last = (int)gridDim.x - 1 - c0;  // slots that exist behind the first
+  const int4 cut = a.head[2 * c0], rows = a.head[2 * c0 + 1];
+  const float2 early = lane <= last ? ml[slot(lane)] : make_float2(-INFINITY, 0.0f);
+  constexpr int kEarly = 4;
+  float part[kEarly][N];
+#pragma unroll
+  for (int i = 0; i < kEarly; ++i) load(min(i, last), part[i]);
+  if (cut.x < 0) return;
+  const int r = cut.z * RG + col;
+  if (r >= a.by_rep.d * rows.y) return;
+  const int n = cut.w - c0 + 1;
+  float top = lane < n ? early.x : -INFINITY;
+  for (int i = lane + 32; i < n; i += 32) top = fmaxf(top, ml[slot(i)].x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   const float ref = top == -INFINITY ? 0.0f : top;
-  constexpr int N = D / 32;
   float sum = 0.0f, acc[N] = {};
   for (int i0 = 0; i0 < n; i0 += 32) {
-    const float2 mine = i0 + lane < n ? ml[slot(i0 + lane)] : make_float2(-INFINITY, 0.0f);
+    const float2 mine = i0 + lane >= n ? make_float2(-INFINITY, 0.0f) : i0 == 0 ? early : ml[slot(i0 + lane)];
     const float by_mine = exp2_fast(mine.x - ref);
     const int here = min(32, n - i0);
-#pragma unroll 4
-    for (int i = 0; i < here; ++i) {
+    auto add = [&](int i, const float (&v)[N]) {
       const float by = __shfl_sync(0xffffffffu, by_mine, i);
       sum = fmaf(__shfl_sync(0xffffffffu, mine.y, i), by, sum);
-      const float *src = a.part + slot(i0 + i) * D + lane * N;
-      if constexpr (N == 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(src);
-        acc[0] = fmaf(v.x, by, acc[0]);
-        acc[1] = fmaf(v.y, by, acc[1]);
-        acc[2] = fmaf(v.z, by, acc[2]);
-        acc[3] = fmaf(v.w, by, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2 *>(src);
-        acc[0] = fmaf(v.x, by, acc[0]);
-        acc[1] = fmaf(v.y, by, acc[1]);
-      }
+#pragma unroll
+      for (int d = 0; d < N; ++d) acc[d] = fmaf(v[d], by, acc[d]);
+    };
+    int i = 0;
+    if (i0 == 0) {
+#pragma unroll
+      for (int k = 0; k < kEarly; ++k)
+        if (k < here) add(k, part[k]);
+      i = kEarly;
+    }
+#pragma unroll 4
+    for (; i < here; ++i) {
+      float v[N];
+      load(i0 + i, v);
+      add(i, v);
     }
   }
-  const int i = r / a.rep, h = cut.y * a.rep + r - i * a.rep;
+  const int i = a.by_rep.quotient(r), h = cut.y * a.by_rep.d + r - i * a.by_rep.d;
   const int64_t row = (int64_t)(rows.x + i) * a.n_q_heads + h;
+  const float by = 1.0f / sum;
 #pragma unroll
-  for (int d = 0; d < N; ++d) store_out(a.out, a.q.dtype, row * D + lane * N + d, acc[d] / sum);
+  for (int d = 0; d < N; d += 2) store2(a.out, a.q.dtype, row * D + dim_of<D>(lane * N + d), acc[d] * by, acc[d + 1] * by);
   if (a.lse && lane == 0) a.lse[row] = (top - p_log2 + log2f(sum)) * kLn2;
 }
 
@@ -952,19 +1018,10 @@ cudaError_t launch(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  kv8_attention_kernel<D, FMT, MODE><<<p.ctas, n_warps(D, MODE) * 32, smem, st>>>(a);
-  e = cudaGetLastError();
+  e = pdl_launch(kv8_attention_kernel<D, FMT, MODE>, dim3(p.ctas), n_warps(D, MODE) * 32, smem, st, a);
   if (e != cudaSuccess || p.pair_mode) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.ctas);
-  cfg.blockDim = dim3(group_rows(MODE) * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<D, group_rows(MODE)>, a, p_log2(FMT, MODE));
+  return pdl_launch(kv8_merge_kernel<D, group_rows(MODE)>, dim3(p.ctas), group_rows(MODE) * 32, 0, st, a,
+                    p_log2(FMT, MODE));
 }
 
 template <int D, int FMT>
@@ -981,9 +1038,11 @@ const char *check_heads(const mk_kv8_cache *c, int n_q_heads, int dtype, const m
   if (n_q_heads / c->n_kv_heads > 1024) return "more than 1024 query heads per kv head";
   if (dtype < MK_F32 || dtype > MK_F16) return "element type must be MK_F32, MK_BF16 or MK_F16";
   if (b->max_rows > MK_KV8_MAX_ROWS) return "max_rows is above MK_KV8_MAX_ROWS";
-  const int64_t chunks = ((int64_t)b->max_pages * c->page_size + kChunk - 1) / kChunk;
-  if (chunks * c->n_kv_heads * ((int64_t)n_q_heads / c->n_kv_heads * b->max_rows + 7) / 8 >= (1ll << 31))
-    return "page tables of so many positions, with so many heads, are not supported";
+  const int64_t chunks = ((int64_t)b->max_pages * c->page_size + kChunk - 1) / kChunk + pair_units(kRows16);
+  const int64_t groups = ((int64_t)n_q_heads / c->n_kv_heads * b->max_rows + 7) / 8;
+  if ((int64_t)c->n_kv_heads * groups >= (1 << 21)) return "so many heads and rows are not supported";
+  if (chunks * c->n_kv_heads * groups * b->n_seqs >= (1ll << 30))
+    return "so many positions (page table entries x heads) are not supported";
   return nullptr;
 }
 
@@ -1001,7 +1060,9 @@ cudaError_t kv8_attention_launch(const mk_kv8_cache &cache, int layer, const mk_
   a.lse = lse;
   a.layer = layer;
   a.n_q_heads = n_q_heads;
-  a.rep = n_q_heads / cache.n_kv_heads;
+  a.by_rep = Divisor(n_q_heads / cache.n_kv_heads);
+  a.by_page = Divisor(cache.page_size);
+  a.by_grid = Divisor(p.ctas);
   a.scale = scale;
   a.block_log2 = __builtin_ctz((unsigned)cache.block);
   a.pair_mode = p.pair_mode;

@@ -163,6 +163,8 @@ __device__ __forceinline__ int find_seq(const mk_batch &b, int t_log2, int slot)
 // of T x D elements.
 template <int FMT, int DT, int PASSES>
 __global__ void __launch_bounds__(256) kv8_store_kernel(const __grid_constant__ StoreArgs a) {
+  pdl_trigger();
+  pdl_wait();
   if (gated(a.gate)) return;
   const int T = a.c.block, P = a.c.page_size, D = a.c.head_dim;
   const int slot = blockIdx.x, which = blockIdx.z;
@@ -274,10 +276,10 @@ cudaError_t launch_store(StoreArgs a, cudaStream_t st) {
   const int heads = warps / split;
   const dim3 grid((unsigned)slots, (unsigned)((a.c.n_kv_heads + heads - 1) / heads), 2);
   const int threads = heads * split * 32;
-  if (passes == 4) kv8_store_kernel<FMT, DT, 4><<<grid, threads, 0, st>>>(a);
-  else if (passes == 8) kv8_store_kernel<FMT, DT, 8><<<grid, threads, 0, st>>>(a);
-  else kv8_store_kernel<FMT, DT, kMost><<<grid, threads, 0, st>>>(a);
-  return cudaGetLastError();
+  const auto kernel = passes == 4   ? kv8_store_kernel<FMT, DT, 4>
+                      : passes == 8 ? kv8_store_kernel<FMT, DT, 8>
+                                    : kv8_store_kernel<FMT, DT, kMost>;
+  return pdl_launch(kernel, grid, threads, 0, st, a);
 }
 
 template <int FMT>

@@ -141,6 +141,8 @@ __device__ __forceinline__ bool bad_entry(const PageArgs &a, int s, int page) {
 // --- fork: a = sources, b = destinations -----------------------------------------
 __global__ void __launch_bounds__(kTeamThreads) fork_kernel(const __grid_constant__ PageArgs a) {
   __shared__ int warps[32];
+  pdl_trigger();
+  pdl_wait();
   Team t = make_team(a, warps);
   const int mp = a.p.max_pages;
   bool bad = false;
@@ -181,6 +183,8 @@ __global__ void __launch_bounds__(kTeamThreads) fork_kernel(const __grid_constan
 // --- free: a = sequences -------------------------------------------------------------
 __global__ void __launch_bounds__(kTeamThreads) free_kernel(const __grid_constant__ PageArgs a) {
   __shared__ int warps[32];
+  pdl_trigger();
+  pdl_wait();
   Team t = make_team(a, warps);
   const int mp = a.p.max_pages;
   bool bad = false;
@@ -244,8 +248,9 @@ struct Walk {
 
 __global__ void __launch_bounds__(kTeamThreads) reserve_kernel(const __grid_constant__ PageArgs a) {
   __shared__ int warps[32];
-  Team t = make_team(a, warps);
   pdl_trigger();
+  pdl_wait();
+  Team t = make_team(a, warps);
   if (t.index() == 0) a.head->copies = 0;
   const int P = a.p.page_size, mp = a.p.max_pages;
   // lengths, and the number of entries before every sequence
@@ -348,8 +353,9 @@ __global__ void __launch_bounds__(kTeamThreads) reserve_kernel(const __grid_cons
 // --- compact --------------------------------------------------------------------------------
 __global__ void __launch_bounds__(kTeamThreads) compact_kernel(const __grid_constant__ PageArgs a) {
   __shared__ int warps[32];
-  Team t = make_team(a, warps);
   pdl_trigger();
+  pdl_wait();
+  Team t = make_team(a, warps);
   if (t.index() == 0) a.head->copies = 0;
   const int64_t entries = (int64_t)a.p.n_seqs * a.p.max_pages;
   bool bad = false;
@@ -400,8 +406,9 @@ __global__ void __launch_bounds__(kTeamThreads) compact_kernel(const __grid_cons
 // --- copy: a = sources, b = destinations ------------------------------------------------------
 __global__ void __launch_bounds__(kTeamThreads) copy_list_kernel(const __grid_constant__ PageArgs a) {
   __shared__ int warps[32];
-  Team t = make_team(a, warps);
   pdl_trigger();
+  pdl_wait();
+  Team t = make_team(a, warps);
   if (t.index() == 0) a.head->copies = 0;
   bool bad = false;
   for (int i = t.index(); i < a.n; i += t.threads()) {
@@ -457,6 +464,7 @@ __device__ __forceinline__ void copy_piece(char *to, const char *from, int bytes
 }
 
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyArgs a) {
+  pdl_trigger();
   pdl_wait();
   const int64_t items = (int64_t)a.head->copies * a.steps;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
@@ -566,12 +574,14 @@ mk_status run_call(const char *name, Kernel kernel, const mk_pages *p, int n, co
   cfg.gridDim = dim3(team);
   cfg.blockDim = dim3(kTeamThreads);
   cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = team;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = team;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
   if (e != cudaSuccess) return ops_cuda_fail(e, name);
   if (!copies || p->n_pools == 0) return MK_OK;
@@ -587,11 +597,8 @@ mk_status run_call(const char *name, Kernel kernel, const mk_pages *p, int n, co
   c.head = a.head;
   c.list = a.list;
   const int64_t most = steps * std::max(n, p->n_pages);
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(most, 4ll * sm_count(p->device)));
-  cfg.blockDim = dim3(kCopyThreads);
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  e = cudaLaunchKernelEx(&cfg, copy_pages_kernel, c);
+  const dim3 grid((unsigned)std::min<int64_t>(most, 4ll * sm_count(p->device)));
+  e = pdl_launch(copy_pages_kernel, grid, kCopyThreads, 0, static_cast<cudaStream_t>(stream), c);
   if (e != cudaSuccess) return ops_cuda_fail(e, name);
   return MK_OK;
 }
