@@ -463,9 +463,11 @@ class _Status:
         if device.type != "cuda":
             _refuse(f"tensors must be on a CUDA device, not {device}")
         self.device, self._index = device, device.index
-        self._i32, self._uint8, self._f32 = torch.int32, torch.uint8, torch.float32
+        self._i32 = torch.int32
         self._raw_stream = torch._C._cuda_getCurrentRawStream
-        self._empty = torch.empty
+        # new tensors on the device, from sizes given one by one: the shortest way
+        self._bytes = torch.empty(0, dtype=torch.uint8, device=device).new_empty
+        self._floats = torch.empty(0, dtype=torch.float32, device=device).new_empty
         self._lib = lib()
 
 
@@ -596,12 +598,11 @@ class KV8Cache(_Status):
             max_rows = 1
         n, max_pages = self._batch(page_table, kv_len, row_start, n_rows, max_rows)
         if out is None:
-            out = self._empty((n_rows, n_heads, self.head_dim), dtype=q.dtype, device=self.device)
+            out = q.new_empty(n_rows, n_heads, self.head_dim)
         elif out.shape != q.shape or out.dtype != q.dtype or out.device != self.device \
                 or not out.is_contiguous():
             _refuse("out must be contiguous, with the shape, type and device of q")
-        lse = self._empty((n_rows, n_heads), dtype=self._f32, device=self.device) \
-            if return_lse else None
+        lse = self._floats(n_rows, n_heads) if return_lse else None
         rq, _, b = self._at
         # the workspace's size follows from the sizes alone
         key = (n_heads, q.dtype, n, max_rows, max_pages)
@@ -614,7 +615,7 @@ class KV8Cache(_Status):
         if n_rows:
             # a workspace of its own for every call: calls on other streams and
             # captured graphs do not meet in it
-            ws = self._empty(size, dtype=self._uint8, device=self.device) if size else None
+            ws = self._bytes(size) if size else None
             rc = self._lib.mk_kv8_attention(
                 self._ref, layer, rq, n_heads, self.head_dim ** -0.5 if scale is None else scale,
                 out.data_ptr(), lse.data_ptr() if return_lse else None, b,
@@ -678,7 +679,7 @@ class PagePool(_Status):
 
     def _call(self, fn, n, args, stream):
         size = self._workspace(n)
-        ws = self._empty(size, dtype=self._uint8, device=self.device)
+        ws = self._bytes(size)
         rc = fn(self._ref, *args, ws.data_ptr(), size, self._stream(stream))
         if rc:
             _check(rc)
