@@ -301,13 +301,17 @@ __device__ __forceinline__ void add_values(const uint8_t *vs_, const int (&v_at)
 #pragma unroll
       for (int c = 0; c < 2; ++c) by[b][j][c] = begin < limit[j][c] ? vs * wc[j][c] : 0.0f;
   }
-  uint32_t vw[kTiles][4][VB / 4];
+  // words at a time: two where two column tiles take up the registers
+  constexpr int VW = MODE == kRows16 ? 2 : VB / 4;
+#pragma unroll
+  for (int w0 = 0; w0 < VB / 4; w0 += VW) {
+  uint32_t vw[kTiles][4][VW];
 #pragma unroll
   for (int tl = 0; tl < kTiles; ++tl)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const uint8_t *vp = vs_ + v_at[r & 1] + (tl * 16 + (r >> 1) * 8) * D;
-      if constexpr (VB == 16) {
+      const uint8_t *vp = vs_ + v_at[r & 1] + (tl * 16 + (r >> 1) * 8) * D + 4 * w0;
+      if constexpr (VW == 4) {
         const uint4 u = *reinterpret_cast<const uint4 *>(vp);
         vw[tl][r][0] = u.x; vw[tl][r][1] = u.y; vw[tl][r][2] = u.z; vw[tl][r][3] = u.w;
       } else {
@@ -316,14 +320,15 @@ __device__ __forceinline__ void add_values(const uint8_t *vs_, const int (&v_at)
       }
     }
 #pragma unroll
-  for (int w = 0; w < VB / 4; ++w) {  // dims 4 w .. 4 w + 3 of the lane: m-tiles 2 w, 2 w + 1
+  for (int wi = 0; wi < VW; ++wi) {
+    const int w = w0 + wi;  // dims 4 w .. 4 w + 3 of the lane: m-tiles 2 w, 2 w + 1
     // the four positions 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of a tile: int8, one
     // word per dim; e4m3, a pair of fp16 for each two
     uint32_t d[kTiles][INT ? 4 : 8];
 #pragma unroll
     for (int tl = 0; tl < kTiles; ++tl) {
-      const uint32_t p = __byte_perm(vw[tl][0][w], vw[tl][1][w], 0x5140), q = __byte_perm(vw[tl][0][w], vw[tl][1][w], 0x7362);
-      const uint32_t r = __byte_perm(vw[tl][2][w], vw[tl][3][w], 0x5140), s = __byte_perm(vw[tl][2][w], vw[tl][3][w], 0x7362);
+      const uint32_t p = __byte_perm(vw[tl][0][wi], vw[tl][1][wi], 0x5140), q = __byte_perm(vw[tl][0][wi], vw[tl][1][wi], 0x7362);
+      const uint32_t r = __byte_perm(vw[tl][2][wi], vw[tl][3][wi], 0x5140), s = __byte_perm(vw[tl][2][wi], vw[tl][3][wi], 0x7362);
       if constexpr (INT) {
         d[tl][0] = __byte_perm(p, r, 0x5410);
         d[tl][1] = __byte_perm(p, r, 0x7632);
@@ -368,6 +373,7 @@ __device__ __forceinline__ void add_values(const uint8_t *vs_, const int (&v_at)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[j][2 * w + h][e] = fmaf(v[e], by[b][j][e & 1], o[j][2 * w + h][e]);
         }
+  }
   }
 }
 

@@ -8,9 +8,17 @@
 // passes are separated by cluster barriers: a grid of independent CTAs would
 // need a launch per pass.  All orders that show in the results come from scans
 // over contiguous runs of entries or pages (thread i of CTA r takes run
-// r * 1024 + i); atomics only count, take minima or maxima.  The copy is bound
-// by HBM (every moved byte is read and written once); the bookkeeping by
-// latency.
+// r * 1024 + i); atomics count, take minima or maxima, or give out room in the
+// copy list, whose order does not matter.
+//
+// The copy is bound by HBM: every moved byte is read and written once, or, where
+// one page is copied for several sequences, read once: their copies lie next to
+// each other in the list and the later reads hit L2.  160 pages of an 8B
+// decoder's 8-bit pools (4.7 MB each) move in 146 us, 32 pages copied three times
+// each take 116 us with the bookkeeping.  The grid is the CTAs that are resident
+// (a call that moves nothing should cost a launch, not thousands of empty CTAs:
+// 64 CTAs per SM cost 9 us more) and takes steps as it goes: SMs differ in their
+// distance to memory, and equal shares took 7 % longer.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -25,13 +33,16 @@ namespace {
 constexpr int kTeamThreads = 1024;
 constexpr int kMaxTeam = 8;             // CTAs of a cluster (the portable limit)
 constexpr int kScans = 8;               // exchanges of one call
-constexpr int kCopyBytes = 32 * 1024;   // a CTA's step of the copy
+constexpr int kCopyBytes = 16 * 1024;   // a CTA's step of the copy
 constexpr int kCopyThreads = 256;
+constexpr int kCopyCtas = 5;            // CTAs per SM of the copy: those that are resident
+constexpr int kNear = 4096;             // sequences, free pages kept in shared memory
 
 // Workspace: the header, then the lists.
 struct Header {
   int copies;  // entries of the copy list
-  int pad[15];
+  int next;    // steps of the copy that have been given out, besides every CTA's first
+  int pad[14];
   int slots[kScans][kMaxTeam];
 };
 
@@ -42,6 +53,7 @@ struct PageArgs {
   int *free_list; // [n_pages]
   int *mark;      // [n_pages]
   int *last;      // [n_pages]
+  int *place;     // [n_pages]
   int *seq;       // [n_seqs + 1]
   int n;
   const int32_t *a, *b;  // the call's two lists
@@ -66,9 +78,8 @@ struct Team {
     i0 = (int)min((int64_t)n, per * index());
     i1 = (int)min((int64_t)n, (int64_t)i0 + per);
   }
-  // Sum of v over the threads before this one; `total` over all.  Orders
-  // everything before it before everything after it, in the whole team.
-  __device__ __forceinline__ int scan(int v, int &total) {
+  // Sum of v over the threads of the CTA before this one; `total` over all.
+  __device__ __forceinline__ int cta_scan(int v, int &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int upto = v;
 #pragma unroll
@@ -89,8 +100,13 @@ struct Team {
       warps[lane] = x;
     }
     __syncthreads();
-    int before = upto - v + (warp ? warps[warp - 1] : 0);
     total = warps[31];
+    return upto - v + (warp ? warps[warp - 1] : 0);
+  }
+  // The same over the team.  Orders everything before it before everything
+  // after it, in the whole team.
+  __device__ __forceinline__ int scan(int v, int &total) {
+    int before = cta_scan(v, total);
     if (size > 1) {
       int *slot = head->slots[used++];
       if (threadIdx.x == 0) __stcg(slot + rank, total);
@@ -105,15 +121,17 @@ struct Team {
     return before;
   }
   // Whether any thread of the team says so; a barrier like scan().
-  __device__ __forceinline__ bool any(bool v) {
-    const int mine = __syncthreads_or(v);
+  __device__ __forceinline__ bool any(bool v) { return any_bits(v ? 1 : 0) != 0; }
+  // The same for two flags.
+  __device__ __forceinline__ int any_bits(int bits) {
+    const int mine = (__syncthreads_or(bits & 1) ? 1 : 0) | (__syncthreads_or(bits & 2) ? 2 : 0);
     if (size == 1) return mine;
     int *slot = head->slots[used++];
     if (threadIdx.x == 0) __stcg(slot + rank, mine);
     cg::this_cluster().sync();
     int all = 0;
     for (int r = 0; r < size; ++r) all |= __ldcg(slot + r);
-    return all != 0;
+    return all;
   }
 };
 
@@ -216,7 +234,6 @@ __global__ void __launch_bounds__(kTeamThreads) free_kernel(const __grid_constan
 // The entries that a call looks at: those whose positions overlap
 // [c, c + n) of some sequence, in the order of sequence and entry.
 struct Walk {
-  const PageArgs &a;
   int s, j, end;  // current sequence, entry, entries of it below `end`
   __device__ __forceinline__ static int first(const PageArgs &a, int s) { return a.a[s] / a.p.page_size; }
   __device__ __forceinline__ static int count(const PageArgs &a, int s) {
@@ -224,20 +241,22 @@ struct Walk {
     if (n <= 0) return 0;
     return (int)(((int64_t)a.a[s] + n + a.p.page_size - 1) / a.p.page_size) - first(a, s);
   }
-  // the e-th entry of the call: seq[s] counts the entries before sequence s
-  __device__ __forceinline__ Walk(const PageArgs &args, int e) : a(args) {
+  // the e-th entry of the call: before[s] counts the entries before sequence s
+  __device__ __forceinline__ void start(const PageArgs &a, const int *before, int e) {
     int lo = 0, hi = a.p.n_seqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (__ldcg(a.seq + mid) <= e) lo = mid;
+      if (before[mid] <= e) lo = mid;
       else hi = mid - 1;
     }
     s = lo;
-    j = first(a, s) + e - __ldcg(a.seq + s);
+    j = first(a, s) + e - before[s];
     end = first(a, s) + count(a, s);
   }
-  __device__ __forceinline__ int32_t *at() const { return a.p.d_page_table + (int64_t)s * a.p.max_pages + j; }
-  __device__ __forceinline__ void next(int e, int e1) {  // to entry e, if there is one
+  __device__ __forceinline__ int32_t *at(const PageArgs &a) const {
+    return a.p.d_page_table + (int64_t)s * a.p.max_pages + j;
+  }
+  __device__ __forceinline__ void next(const PageArgs &a, int e, int e1) {  // to entry e, if there is one
     if (e >= e1) return;
     if (++j < end) return;
     do ++s; while (count(a, s) == 0);
@@ -248,14 +267,21 @@ struct Walk {
 
 __global__ void __launch_bounds__(kTeamThreads) reserve_kernel(const __grid_constant__ PageArgs a) {
   __shared__ int warps[32];
+  __shared__ int near_seq[kNear], near_free[kNear];
   pdl_trigger();
   pdl_wait();
   Team t = make_team(a, warps);
-  if (t.index() == 0) a.head->copies = 0;
+  if (t.index() == 0) a.head->copies = a.head->next = 0;
   const int P = a.p.page_size, mp = a.p.max_pages;
-  // lengths, and the number of entries before every sequence
-  int s0, s1;
-  t.run(a.p.n_seqs, s0, s1);
+  // free pages of this thread's run (the counts change only at the end)
+  int p0, p1;
+  t.run(a.p.n_pages, p0, p1);
+  int n_free = 0;
+  for (int p = p0; p < p1; ++p) n_free += a.p.d_ref[p] == 0;
+  // lengths, and the number of entries before every sequence: every CTA for itself
+  int *before = a.p.n_seqs <= kNear ? near_seq : a.seq;
+  const int per = (a.p.n_seqs + kTeamThreads - 1) / kTeamThreads;
+  const int s0 = min(a.p.n_seqs, (int)threadIdx.x * per), s1 = min(a.p.n_seqs, s0 + per);
   bool bad = false;
   int mine = 0;
   for (int s = s0; s < s1; ++s) {
@@ -267,40 +293,42 @@ __global__ void __launch_bounds__(kTeamThreads) reserve_kernel(const __grid_cons
       mine += Walk::count(a, s);
     }
   }
-  if (t.any(bad)) return;
   int entries;
-  int before = t.scan(mine, entries);
+  int upto = t.cta_scan(mine, entries);
   for (int s = s0; s < s1; ++s) {
-    __stcg(a.seq + s, before);
-    before += Walk::count(a, s);
+    before[s] = upto;
+    upto += bad ? 0 : Walk::count(a, s);
   }
-  t.sync();
+  if (__syncthreads_or(bad)) return;  // all CTAs have seen the same lengths
   int e0, e1;
   t.run(entries, e0, e1);
+  Walk from{0, 0, 0};
+  if (e0 < e1) from.start(a, before, e0);
   // a shared page: how many of its holders write it, and the last of them
-  if (e0 < e1) {
-    Walk w(a, e0);
-    for (int e = e0; e < e1; w.next(++e, e1)) {
-      const int page = *w.at();
-      if (bad_entry(a, w.s, page)) bad = true;
-      else if (page >= 0 && a.p.d_ref[page] > 1) {
-        __stcg(a.mark + page, 0);
-        __stcg(a.last + page, -1);
-      }
+  bool shared = false;
+  Walk w = from;
+  for (int e = e0; e < e1; w.next(a, ++e, e1)) {
+    const int page = *w.at(a);
+    if (bad_entry(a, w.s, page)) bad = true;
+    else if (page >= 0 && a.p.d_ref[page] > 1) {
+      shared = true;
+      __stcg(a.mark + page, 0);
+      __stcg(a.last + page, -1);
     }
   }
-  if (t.any(bad)) return;
-  if (e0 < e1) {
-    Walk w(a, e0);
-    for (int e = e0; e < e1; w.next(++e, e1)) {
-      const int page = *w.at();
+  const int seen = t.any_bits((bad ? 1 : 0) | (shared ? 2 : 0));
+  if (seen & 1) return;
+  if (seen & 2) {
+    w = from;
+    for (int e = e0; e < e1; w.next(a, ++e, e1)) {
+      const int page = *w.at(a);
       if (page >= 0 && a.p.d_ref[page] > 1) {
         atomicAdd(a.mark + page, 1);
         atomicMax(a.last + page, e);
       }
     }
+    t.sync();
   }
-  t.sync();
   // an entry gets a free page if it has none, or if its page is shared and it
   // is not the last writer of a page that all its holders write
   auto shared_write = [&](int page, int e) {
@@ -308,46 +336,49 @@ __global__ void __launch_bounds__(kTeamThreads) reserve_kernel(const __grid_cons
     return refs > 1 && !(__ldcg(a.mark + page) == refs && __ldcg(a.last + page) == e);
   };
   int need = 0;
-  if (e0 < e1) {
-    Walk w(a, e0);
-    for (int e = e0; e < e1; w.next(++e, e1)) {
-      const int page = *w.at();
-      if (page < 0 || shared_write(page, e)) ++need;
+  w = from;
+  for (int e = e0; e < e1; w.next(a, ++e, e1)) {
+    const int page = *w.at(a);
+    if (page < 0 || shared_write(page, e)) ++need;
+    if (page >= 0 && a.p.d_ref[page] > 1 && __ldcg(a.last + page) == e) {
+      // one writer takes room in the copy list for all of the page's, so that
+      // copies of one page are made at the same time and it is read once
+      const int writers = __ldcg(a.mark + page);
+      __stcg(a.place + page, atomicAdd(&a.head->copies, writers - (writers == a.p.d_ref[page])));
     }
   }
   int all_need, all_free;
   int at = t.scan(need, all_need);
-  int p0, p1;
-  t.run(a.p.n_pages, p0, p1);
-  int n_free = 0;
-  for (int p = p0; p < p1; ++p) n_free += a.p.d_ref[p] == 0;
   int k = t.scan(n_free, all_free);
   if (all_free < all_need) {
     if (t.index() == 0)
       record_status(a.p.d_status, MK_ERR_OOM, a.p.n_pages, all_need - all_free, MK_CHECK_FREE);
     return;
   }
+  if (all_need == 0) return;
+  int *free_list = t.size == 1 && all_need <= kNear ? near_free : a.free_list;
   for (int p = p0; p < p1 && k < all_need; ++p)
-    if (a.p.d_ref[p] == 0) __stcg(a.free_list + k++, p);
+    if (a.p.d_ref[p] == 0) free_list[k++] = p;
   t.sync();
-  if (e0 < e1) {
-    Walk w(a, e0);
-    for (int e = e0; e < e1; w.next(++e, e1)) {
-      const int page = *w.at();
-      if (page >= 0 && !shared_write(page, e)) continue;
-      const int fresh = __ldcg(a.free_list + at++);
-      *w.at() = fresh;
-      if (page >= 0) {
-        // contents matter if the page holds positions before the new ones
-        const bool copy = (int64_t)w.j * P < a.a[w.s];
-        a.list[atomicAdd(&a.head->copies, 1)] = make_int2(page, copy ? fresh : ~fresh);
-      }
+  w = from;
+  for (int e = e0; e < e1; w.next(a, ++e, e1)) {
+    const int page = *w.at(a);
+    if (page >= 0 && !shared_write(page, e)) continue;
+    const int fresh = free_list == near_free ? near_free[at++] : __ldcg(a.free_list + at++);
+    *w.at(a) = fresh;
+    if (page >= 0) {
+      // contents matter if the page holds positions before the new ones
+      const bool copy = (int64_t)w.j * P < a.a[w.s];
+      a.list[atomicAdd(a.place + page, 1)] = make_int2(page, copy ? fresh : ~fresh);
     }
   }
   t.sync();
-  for (int i = t.index(); i < all_need; i += t.threads()) a.p.d_ref[__ldcg(a.free_list + i)] = 1;
-  const int given_up = __ldcg(&a.head->copies);
-  for (int i = t.index(); i < given_up; i += t.threads()) atomicSub(a.p.d_ref + __ldcg(&a.list[i].x), 1);
+  for (int i = t.index(); i < all_need; i += t.threads())
+    a.p.d_ref[free_list == near_free ? near_free[i] : __ldcg(a.free_list + i)] = 1;
+  if (seen & 2) {
+    const int given_up = __ldcg(&a.head->copies);
+    for (int i = t.index(); i < given_up; i += t.threads()) atomicSub(a.p.d_ref + __ldcg(&a.list[i].x), 1);
+  }
 }
 
 // --- compact --------------------------------------------------------------------------------
@@ -356,7 +387,7 @@ __global__ void __launch_bounds__(kTeamThreads) compact_kernel(const __grid_cons
   pdl_trigger();
   pdl_wait();
   Team t = make_team(a, warps);
-  if (t.index() == 0) a.head->copies = 0;
+  if (t.index() == 0) a.head->copies = a.head->next = 0;
   const int64_t entries = (int64_t)a.p.n_seqs * a.p.max_pages;
   bool bad = false;
   for (int64_t e = t.index(); e < entries; e += t.threads()) {
@@ -409,7 +440,7 @@ __global__ void __launch_bounds__(kTeamThreads) copy_list_kernel(const __grid_co
   pdl_trigger();
   pdl_wait();
   Team t = make_team(a, warps);
-  if (t.index() == 0) a.head->copies = 0;
+  if (t.index() == 0) a.head->copies = a.head->next = 0;
   bool bad = false;
   for (int i = t.index(); i < a.n; i += t.threads()) {
     const int from = a.a[i], to = a.b[i];
@@ -441,7 +472,7 @@ struct CopyArgs {
   int n_pools, steps;                  // steps: of kCopyBytes, of one page over all pools
   char *pool[MK_MAX_POOLS];
   int64_t bytes[MK_MAX_POOLS];
-  const Header *head;
+  Header *head;
   const int2 *list;
 };
 
@@ -456,9 +487,9 @@ __device__ __forceinline__ void copy_piece(char *to, const char *from, int bytes
   for (; i + (kUnroll - 1) * kCopyThreads < n; i += kUnroll * kCopyThreads) {
     V v[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) v[u] = __ldcs(s + i + u * kCopyThreads);
+    for (int u = 0; u < kUnroll; ++u) v[u] = __ldg(s + i + u * kCopyThreads);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) __stcs(d + i + u * kCopyThreads, v[u]);
+    for (int u = 0; u < kUnroll; ++u) d[i + u * kCopyThreads] = v[u];
   }
   for (; i < n; i += kCopyThreads) d[i] = s[i];
 }
@@ -467,25 +498,32 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
   pdl_trigger();
   pdl_wait();
   const int64_t items = (int64_t)a.head->copies * a.steps;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+  __shared__ int upcoming;
+  for (int64_t item = blockIdx.x; item < items;) {
+    // SMs are not equally fast: a CTA takes the next step that is left
+    if (threadIdx.x == 0) upcoming = atomicAdd(&a.head->next, 1);
     const int i = (int)(item / a.steps);
     int step = (int)(item - (int64_t)i * a.steps);
     const int2 pair = a.list[i];
-    if (pair.y < 0) continue;  // a page that is replaced without its contents
-    int pool = 0;
-    for (;; ++pool) {
-      const int n = (int)((a.bytes[pool] + kCopyBytes - 1) / kCopyBytes);
-      if (step < n) break;
-      step -= n;
+    if (pair.y >= 0) {  // else a page that is replaced without its contents
+      int pool = 0;
+      for (;; ++pool) {
+        const int n = (int)((a.bytes[pool] + kCopyBytes - 1) / kCopyBytes);
+        if (step < n) break;
+        step -= n;
+      }
+      const int64_t size = a.bytes[pool], off = (int64_t)step * kCopyBytes;
+      const int bytes = (int)min((int64_t)kCopyBytes, size - off);
+      char *to = a.pool[pool] + pair.y * size + off;
+      const char *from = a.pool[pool] + pair.x * size + off;
+      if ((size & 15) == 0 && (reinterpret_cast<uintptr_t>(a.pool[pool]) & 15) == 0)
+        copy_piece<uint4>(to, from, bytes);
+      else
+        copy_piece<uint32_t>(to, from, bytes);
     }
-    const int64_t size = a.bytes[pool], off = (int64_t)step * kCopyBytes;
-    const int bytes = (int)min((int64_t)kCopyBytes, size - off);
-    char *to = a.pool[pool] + pair.y * size + off;
-    const char *from = a.pool[pool] + pair.x * size + off;
-    if ((size & 15) == 0 && (reinterpret_cast<uintptr_t>(a.pool[pool]) & 15) == 0)
-      copy_piece<uint4>(to, from, bytes);
-    else
-      copy_piece<uint32_t>(to, from, bytes);
+    __syncthreads();
+    item = (int64_t)gridDim.x + upcoming;
+    __syncthreads();
   }
 }
 
@@ -495,7 +533,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
 int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
 
 struct Places {
-  int64_t list, free_list, mark, last, seq, total;
+  int64_t list, free_list, mark, last, place, seq, total;
 };
 Places places(const mk_pages &p, int n) {
   Places w{};
@@ -507,6 +545,8 @@ Places places(const mk_pages &p, int n) {
   w.mark = off;
   off += up16(4ll * p.n_pages);
   w.last = off;
+  off += up16(4ll * p.n_pages);
+  w.place = off;
   off += up16(4ll * p.n_pages);
   w.seq = off;
   off += up16(4ll * (p.n_seqs + 1));
@@ -565,6 +605,7 @@ mk_status run_call(const char *name, Kernel kernel, const mk_pages *p, int n, co
   a.free_list = reinterpret_cast<int *>(base + w.free_list);
   a.mark = reinterpret_cast<int *>(base + w.mark);
   a.last = reinterpret_cast<int *>(base + w.last);
+  a.place = reinterpret_cast<int *>(base + w.place);
   a.seq = reinterpret_cast<int *>(base + w.seq);
   a.n = n;
   a.a = static_cast<const int32_t *>(list_a);
@@ -597,7 +638,7 @@ mk_status run_call(const char *name, Kernel kernel, const mk_pages *p, int n, co
   c.head = a.head;
   c.list = a.list;
   const int64_t most = steps * std::max(n, p->n_pages);
-  const dim3 grid((unsigned)std::min<int64_t>(most, 4ll * sm_count(p->device)));
+  const dim3 grid((unsigned)std::min<int64_t>(most, (int64_t)kCopyCtas * sm_count(p->device)));
   e = pdl_launch(copy_pages_kernel, grid, kCopyThreads, 0, static_cast<cudaStream_t>(stream), c);
   if (e != cudaSuccess) return ops_cuda_fail(e, name);
   return MK_OK;
