@@ -38,11 +38,12 @@
 //
 // Work split.  The (sequence, kv head, row group) pairs, each with
 // ceil(length / kChunk) chunks, lie end to end on one line that the grid cuts
-// into equal pieces, from the device's own lengths; a pair that crosses a cut
+// into equal pieces, from the device's own lengths, unless whole pairs come out
+// nearly as even; a pair that crosses a cut
 // leaves partial results (o, max, sum) in the workspace and a second, small
 // launch adds them up in a fixed order.  Where the page table is so short that
-// a pair is at most kPairChunks chunks, a CTA takes one whole pair instead and
-// the second launch is left out.
+// a pair is at most kPairChunks chunks, a CTA takes one whole pair and the second
+// launch is left out.
 #include <cuda_fp16.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -58,7 +59,8 @@ namespace {
 
 constexpr int kChunk = 32;            // positions of a warp's step
 constexpr int kTiles = kChunk / 16;   // 16-position MMA tiles of a chunk
-constexpr int kPairChunks = 16;       // longest pair (in chunks) that one CTA takes whole
+constexpr int kPairChunks = 32;       // longest pair (in chunks) for which nothing is ever cut
+constexpr int kCutUnits = 8;          // what cutting costs a CTA, in chunks
 constexpr int kMinUnits = 4;          // shortest piece of the cut line, in units (chunks)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -110,9 +112,12 @@ struct AttnArgs {
 
 constexpr int group_rows(int mode) { return mode == kRows16 ? 16 : 8; }
 
-// Warps of a CTA and CTAs per SM: as many as their registers allow.
-__host__ __device__ constexpr int n_warps(int, int mode) { return mode == kRows8F32 ? 4 : 8; }
-__host__ __device__ constexpr int n_ctas(int, int mode) { return mode == kRows8F32 ? 2 : 1; }
+// A CTA has 8 warps and an SM to itself, or 4 warps and half of one; their
+// registers allow no more.  Cut lines: 8 (one long sequence of e4m3 56 us against
+// 59), with fp32 rows 4 (batch 8 22.5 against 26).  Whole pairs: 8 while every
+// pair has an SM to itself (one sequence of 250: 6.2 us against 8), else 4, whose
+// fixed costs overlap (64 sequences of 250: 16 us against 20.6).
+__host__ __device__ constexpr int ctas_per_sm(int warps) { return warps == 4 ? 2 : 1; }
 
 // What a pair costs a CTA besides its chunks (query rows, the warps' results),
 // in units of a chunk.
@@ -137,13 +142,13 @@ __host__ __device__ constexpr float p_log2(int fmt, int mode) {
 // Shared memory: for each warp a slot for a chunk's K codes and scales and one
 // for V (later the warps' results), then the query rows' terms.
 __host__ __device__ constexpr int slot_bytes(int D) { return kChunk * D + 16; }
-__host__ __device__ constexpr int q_offset(int D, int mode) {
-  const int ring = n_warps(D, mode) * 2 * slot_bytes(D);
-  const int merge = n_warps(D, mode) * group_rows(mode) * (D + 4) * 4;
+__host__ __device__ constexpr int q_offset(int D, int mode, int warps) {
+  const int ring = warps * 2 * slot_bytes(D);
+  const int merge = warps * group_rows(mode) * (D + 4) * 4;
   return ring > merge ? ring : merge;
 }
-__host__ __device__ constexpr int smem_bytes(int D, int fmt, int mode) {
-  return q_offset(D, mode) + q_terms(fmt, mode) * group_rows(mode) * D * (fmt == MK_KV8_INT8 ? 1 : 2);
+__host__ __device__ constexpr int smem_bytes(int D, int fmt, int mode, int warps) {
+  return q_offset(D, mode, warps) + q_terms(fmt, mode) * group_rows(mode) * D * (fmt == MK_KV8_INT8 ? 1 : 2);
 }
 
 // Codes of a chunk in a slot: as in the cache, but with the eight 16-byte
@@ -380,11 +385,10 @@ __device__ __forceinline__ void add_values(const uint8_t *vs_, const int (&v_at)
 // Chunks [k0, k1) of pair (sequence q.s, kv head hk, row group g) by one CTA;
 // `whole`: they are all of it and the result is final, else it goes to
 // partial slot `slot`.
-template <int D, int FMT, int MODE>
+template <int D, int FMT, int MODE, int W>
 __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, const SeqRows &q,
                                             int hk, int g, int k0, int k1, bool whole, int slot) {
   constexpr bool INT = FMT == MK_KV8_INT8;
-  constexpr int W = n_warps(D, MODE);
   constexpr int RG = group_rows(MODE);
   constexpr int NO = MODE == kRows16 ? 2 : 1;            // column tiles of 8 rows
   constexpr int NQ = q_terms(FMT, MODE), NP = p_terms(FMT, MODE);
@@ -464,7 +468,7 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
   // --- query rows, once for all warps: a warp quantises a row at a time ------
   constexpr int QB = INT ? 1 : 2;  // bytes of a term
   constexpr int NR = (RG + W - 1) / W;
-  uint8_t *qs = smem + q_offset(D, MODE);  // [term][row][D]
+  uint8_t *qs = smem + q_offset(D, MODE, W);  // [term][row][D]
   float x_row[NR][D / 32];
   int lim_row[NR];
 #pragma unroll
@@ -818,8 +822,8 @@ __device__ __forceinline__ SeqLine seq_line(const AttnArgs &a, const SeqRows &q)
   return {chunks, groups, (chunks + pair_units(MODE)) * groups * a.c.n_kv_heads};
 }
 
-template <int D, int FMT, int MODE>
-__global__ void __launch_bounds__(n_warps(D, MODE) * 32, n_ctas(D, MODE)) kv8_attention_kernel(const __grid_constant__ AttnArgs a) {
+template <int D, int FMT, int MODE, int W>
+__global__ void __launch_bounds__(W * 32, ctas_per_sm(W)) kv8_attention_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_trigger();  // the launch behind this one may get ready; it waits for this grid's end
   pdl_wait();
@@ -830,7 +834,7 @@ __global__ void __launch_bounds__(n_warps(D, MODE) * 32, n_ctas(D, MODE)) kv8_at
     const SeqRows q = seq_rows(a.b, a.c.page_size, s);
     const SeqLine y = seq_line<MODE>(a, q);
     if (q.bad && hk == 0 && g == 0 && threadIdx.x == 0) reject(a, q);
-    if (g < y.groups) run_segment<D, FMT, MODE>(a, smem, q, hk, g, 0, y.chunks, true, 0);
+    if (g < y.groups) run_segment<D, FMT, MODE, W>(a, smem, q, hk, g, 0, y.chunks, true, 0);
     return;
   }
   // The line: every warp adds up all sequences, 32 at a time, and finds the one
@@ -840,6 +844,7 @@ __global__ void __launch_bounds__(n_warps(D, MODE) * 32, n_ctas(D, MODE)) kv8_at
   SeqLine line;
   int upto;       // units of the sequences s0 .. s0 + lane
   int s0;
+  bool whole = false;  // nothing is cut: a pair is one unit, and the pieces are dealt out
   auto group = [&](int first) {
     s0 = first;
     line = SeqLine{0, 0, 0};
@@ -847,6 +852,7 @@ __global__ void __launch_bounds__(n_warps(D, MODE) * 32, n_ctas(D, MODE)) kv8_at
     if (first + lane < a.b.n_seqs) {
       mine = seq_rows(a.b, a.c.page_size, first + lane);
       line = seq_line<MODE>(a, mine);
+      if (whole) line.units = line.groups * a.c.n_kv_heads;
     }
     upto = line.units;
 #pragma unroll
@@ -855,23 +861,26 @@ __global__ void __launch_bounds__(n_warps(D, MODE) * 32, n_ctas(D, MODE)) kv8_at
       if (lane >= d) upto += v;
     }
   };
-  int total = 0;
+  int total = 0, pairs = 0, longest = 0;
   for (int first = 0; first < a.b.n_seqs; first += 32) {
     group(first);
     if (mine.bad && threadIdx.x < 32 && mine.s % (int)gridDim.x == (int)blockIdx.x) reject(a, mine);
     total += __shfl_sync(0xffffffffu, upto, 31);
+    pairs += __reduce_add_sync(0xffffffffu, line.groups * a.c.n_kv_heads);
+    longest = max(longest, __reduce_max_sync(0xffffffffu, line.chunks));
   }
   // the host allows fewer than 2^30 units
   const int per = max(kMinUnits, a.by_grid.quotient(total + (int)gridDim.x - 1));
-  const int u0 = (int)min((int64_t)total, (int64_t)per * blockIdx.x), u1 = min(total, u0 + per);
+  // Whole pairs where the busiest CTA's share is at most 4/3 of an equal one and
+  // a bit: an SM alone draws 4/3 of its share of the HBM rate, and cutting
+  // costs partial results and their sums (16 sequences of 1024: 14.6 us whole,
+  // 18.5 cut; 8 of 256 to 4096: 34.9 whole, 16.5 cut).
+  const int64_t busiest = (int64_t)a.by_grid.quotient(pairs + (int)gridDim.x - 1) * (longest + pair_units(MODE));
+  whole = 3 * busiest <= 4 * ((int64_t)per + kCutUnits);
+  const int u0 = whole ? (int)blockIdx.x : (int)min((int64_t)total, (int64_t)per * blockIdx.x);
+  const int u1 = whole ? pairs : min(total, u0 + per);
   int base0 = 0;  // units before sequence s0
-  if (a.b.n_seqs > 32 && u0 < u1) {
-    group(0);
-    while (u0 >= base0 + __shfl_sync(0xffffffffu, upto, 31)) {
-      base0 += __shfl_sync(0xffffffffu, upto, 31);
-      group(s0 + 32);
-    }
-  }
+  if ((whole || a.b.n_seqs > 32) && u0 < u1) group(0);
   int4 cut = make_int4(-1, 0, 0, 0), cut2 = make_int4(0, 0, 0, 0);
   int u = u0;
   while (u < u1) {
@@ -888,20 +897,20 @@ __global__ void __launch_bounds__(n_warps(D, MODE) * 32, n_ctas(D, MODE)) kv8_at
     const int chunks = __shfl_sync(0xffffffffu, line.chunks, at);
     const int groups = __shfl_sync(0xffffffffu, line.groups, at);
     const int base = base0 + __shfl_sync(0xffffffffu, upto - line.units, at);
-    const int len = chunks + pair_units(MODE);
+    const int len = whole ? 1 : chunks + pair_units(MODE);
     const int pair = small_quotient(u - base, len), k0 = u - base - pair * len;
-    const int k1 = min(chunks, k0 + u1 - u);
+    const int k1 = whole ? chunks : min(chunks, k0 + u1 - u);
     if (k0 < chunks) {
       const int hk = groups == 1 ? pair : small_quotient(pair, groups), g = pair - hk * groups;
-      const bool whole = k0 == 0 && k1 == chunks;
-      run_segment<D, FMT, MODE>(a, smem, q, hk, g, k0, k1, whole, 2 * (int)blockIdx.x + (k0 == 0 ? 1 : 0));
-      if (k0 == 0 && !whole) {
+      const bool all = k0 == 0 && k1 == chunks;
+      run_segment<D, FMT, MODE, W>(a, smem, q, hk, g, k0, k1, all, 2 * (int)blockIdx.x + (k0 == 0 ? 1 : 0));
+      if (k0 == 0 && !all) {
         // the pair goes on in the CTAs behind this one, to that of its last chunk
         cut = make_int4(q.s, hk, g, small_quotient(base + pair * len + chunks - 1, per));
         cut2 = make_int4(q.r0, q.n, 0, 0);
       }
     }
-    u = base + (pair + 1) * len;  // the next pair, if the piece goes that far
+    u = whole ? u + (int)gridDim.x : base + (pair + 1) * len;  // the next pair, if the piece goes that far
   }
   if (threadIdx.x == 0) {
     a.head[2 * blockIdx.x] = cut;
@@ -988,7 +997,7 @@ int mode_of(int dtype, int rep, int max_rows) {
 
 // Grid and workspace of a call, from what the host knows.
 struct AttnPlan {
-  int mode, groups, ctas;
+  int mode, groups, ctas, warps;
   bool pair_mode;
   int64_t bytes;
 };
@@ -1002,32 +1011,39 @@ AttnPlan plan_of(const mk_kv8_cache &c, const mk_batch &b, int n_q_heads, int dt
   const int64_t pairs = (int64_t)b.n_seqs * c.n_kv_heads * p.groups;
   const int64_t chunks = ((int64_t)b.max_pages * c.page_size + kChunk - 1) / kChunk;
   p.pair_mode = chunks <= kPairChunks && pairs < (1ll << 30);
+  const int sms = sm_count(c.device);
   if (p.pair_mode) {
     p.ctas = (int)pairs;
+    p.warps = pairs <= sms ? 8 : 4;
     return p;
   }
-  const int sms = sm_count(c.device);
-  p.ctas = (int)std::min<int64_t>((int64_t)sms * n_ctas(c.head_dim, p.mode), (pairs * chunks + kMinUnits - 1) / kMinUnits);
+  p.warps = p.mode == kRows8F32 ? 4 : 8;
+  p.ctas = (int)std::min<int64_t>((int64_t)sms * ctas_per_sm(p.warps), (pairs * chunks + kMinUnits - 1) / kMinUnits);
   p.bytes = (int64_t)p.ctas * (32 + 2 * rg * 8 + 2ll * rg * c.head_dim * 4);
   return p;
 }
 
-template <int D, int FMT, int MODE>
+template <int D, int FMT, int MODE, int W>
 cudaError_t launch(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
-  constexpr int smem = smem_bytes(D, FMT, MODE);
+  constexpr int smem = smem_bytes(D, FMT, MODE, W);
   static std::atomic<uint64_t> ready{0};  // devices whose limit has been raised
   const uint64_t bit = a.c.device < 64 ? 1ull << a.c.device : 0;
   cudaError_t e = cudaSuccess;
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kv8_attention_kernel<D, FMT, MODE>,
+    e = cudaFuncSetAttribute(kv8_attention_kernel<D, FMT, MODE, W>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  e = pdl_launch(kv8_attention_kernel<D, FMT, MODE>, dim3(p.ctas), n_warps(D, MODE) * 32, smem, st, a);
+  e = pdl_launch(kv8_attention_kernel<D, FMT, MODE, W>, dim3(p.ctas), W * 32, smem, st, a);
   if (e != cudaSuccess || p.pair_mode) return e;
   return pdl_launch(kv8_merge_kernel<D, group_rows(MODE)>, dim3(p.ctas), group_rows(MODE) * 32, 0, st, a,
                     p_log2(FMT, MODE));
+}
+
+template <int D, int FMT, int MODE>
+cudaError_t launch(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
+  return p.warps == 4 ? launch<D, FMT, MODE, 4>(a, p, st) : launch<D, FMT, MODE, 8>(a, p, st);
 }
 
 template <int D, int FMT>
