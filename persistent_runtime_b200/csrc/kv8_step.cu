@@ -36,7 +36,9 @@ __device__ __forceinline__ float bf(uint16_t h) { return __uint_as_float((uint32
 // One CTA per sequence and kv head, one warp per row of its group.  Bound by
 // latency: a few KB per CTA.
 template <int D>
-__global__ void __launch_bounds__(256) qkv_norm_rope(const RopeArgs a) {
+__global__ void __launch_bounds__(256) qkv_norm_rope(const __grid_constant__ RopeArgs a) {
+  pdl_trigger();
+  pdl_wait();
   if (*(volatile const int32_t *)a.status != 0) return;
   const int g = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 31;
   const int pos = a.kv_len[b];
@@ -96,6 +98,8 @@ __device__ __forceinline__ uint16_t to_bf(float f) {  // round to nearest even
 // the worker kernel's B fragments.
 __global__ void attention_operand(const float *att, uint16_t *opnd, int K, int nn,
                                   const int32_t *status) {
+  pdl_trigger();
+  pdl_wait();
   const int k = blockIdx.x * blockDim.x + threadIdx.x, b = blockIdx.y, kk = k & 15;
   if (k >= K || *(volatile const int32_t *)status != 0) return;
   const float x = att[(int64_t)b * K + k];
@@ -216,17 +220,15 @@ extern "C" mk_status mk_decode_step_kv8(mk_handle *h, const int32_t *d_tokens_in
                        m.n_kv_heads, rep, m.kv_capacity, c.page_size, max_pages, c.n_pages, first, m.rms_eps};
       first = false;
       const dim3 grid(m.n_kv_heads, m.batch);
-      if (D == 128) qkv_norm_rope<128><<<grid, 256, 0, st>>>(r);
-      else qkv_norm_rope<64><<<grid, 256, 0, st>>>(r);
-      e = cudaGetLastError();
+      e = pdl_launch(D == 128 ? qkv_norm_rope<128> : qkv_norm_rope<64>, grid, 256, 0, st, r);
       if (e == cudaSuccess) e = kv8_store_launch(c, layer, k_rows, v_rows, batch, p.status, st);
       if (e == cudaSuccess)
         e = kv8_attention_launch(c, layer, q_rows, m.n_q_heads, p.attn_scale, m.batch > 1 ? att : L.att,
                                  nullptr, batch, base + w.attention, p.status, st);
       if (e == cudaSuccess && m.batch > 1) {
         const int K = m.n_q_heads * D;
-        attention_operand<<<dim3((K + 255) / 256, m.batch), 256, 0, st>>>(att, L.attb, K, p.nn, p.status);
-        e = cudaGetLastError();
+        e = pdl_launch(attention_operand, dim3((K + 255) / 256, m.batch), 256, 0, st, (const float *)att, L.attb, K,
+                       p.nn, (const int32_t *)p.status);
       }
     }
     if (e != cudaSuccess) {
