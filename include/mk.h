@@ -456,7 +456,7 @@ mk_status mk_kv8_store(const mk_kv8_cache *cache, int layer, const mk_rows *k, c
  * `layer` of the cache: row i of sequence s sees the positions
  * 0 .. kv_len[s] + i, its own included (store the call's K/V rows first).
  * Head h reads kv head h / (n_q_heads / n_kv_heads).  d_out [n_rows][n_q_heads]
- * [head_dim], contiguous and 16-byte aligned, has the element type of q;
+ * [head_dim], contiguous, 16-byte aligned and apart from q, has its element type;
  * d_lse [n_rows][n_q_heads] (or NULL) receives log(sum(exp(scores))).  Rows
  * outside every sequence are not written.  Codes enter the products exactly,
  * sums and softmax are fp32 (int8 products: exact integers).  A query element

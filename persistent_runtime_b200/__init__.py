@@ -479,7 +479,8 @@ class KV8Cache(_Status):
     k_scale, v_scale  float32 [n_pages][n_layers][n_kv_heads][page_size / block]
 
     The pages belong to sequences as in Megakernel.decode_steps_paged: position p of sequence s
-    is row p % page_size of page page_table[s][p // page_size]."""
+    is row p % page_size of page page_table[s][p // page_size].  Calls are asynchronous on the
+    current (or the given) stream of the cache's device; use one object per thread."""
 
     def __init__(self, k, v, k_scale, v_scale):
         import torch
@@ -600,8 +601,8 @@ class KV8Cache(_Status):
         if out is None:
             out = q.new_empty(n_rows, n_heads, self.head_dim)
         elif out.shape != q.shape or out.dtype != q.dtype or out.device != self.device \
-                or not out.is_contiguous():
-            _refuse("out must be contiguous, with the shape, type and device of q")
+                or not out.is_contiguous() or out.data_ptr() == q.data_ptr():
+            _refuse("out must be contiguous, with the shape, type and device of q, and not q itself")
         lse = self._floats(n_rows, n_heads) if return_lse else None
         rq, _, b = self._at
         # the workspace's size follows from the sizes alone
@@ -633,7 +634,9 @@ class PagePool(_Status):
     page_table  int32 [n_seqs][max_pages], -1 = no page
     ref_count   int32 [n_pages], page table entries that name the page
     pools       tensors whose first dimension are the pages: the K and V pools of
-                Megakernel.decode_steps_paged, or KV8Cache.pools()"""
+                Megakernel.decode_steps_paged, or KV8Cache.pools()
+
+    Calls are asynchronous, like KV8Cache's; use one object per thread."""
 
     def __init__(self, page_table, ref_count, page_size, pools):
         self._bind(page_table.device)

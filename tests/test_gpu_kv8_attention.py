@@ -147,6 +147,37 @@ def test_strides_bounds_and_repeats():
         assert t.equal(cache.attention(1, q.cuda(), *args, row_start=dev(start), max_rows=3), want)
 
 
+def test_the_binding_refuses():
+    import persistent_runtime_b200 as prb
+    t = torch()
+    case = (4, 2, 64, 32, 16, "int8", "bfloat16", [40, 50], [1, 1])
+    host, q, table, cached, new, start = setup(case, 18)
+    cache = host.device()
+    q, table, lens, start = q.cuda(), dev(table), dev(cached.astype(np.int32)), dev(start)
+    k = t.zeros(2, 2, 64, device="cuda")
+    bad = [lambda: cache.attention(1, q, table, lens, out=q), lambda: cache.attention(1, q.double(), table, lens),
+           lambda: cache.attention(1, q, table.long(), lens), lambda: cache.attention(1, q, table, lens[:1]),
+           lambda: cache.attention(1, q[:, :, :32], table, lens), lambda: cache.attention(1, q[:1], table, lens),
+           lambda: cache.attention(1, q, table, lens, row_start=start), lambda: cache.attention(2, q, table, lens),
+           lambda: cache.attention(1, q, table, lens, row_start=start, max_rows=17),
+           lambda: cache.attention(1, q, table[:, ::2], lens), lambda: cache.attention(1, q[:, :3], table, lens),
+           lambda: cache.attention(1, q.cpu(), table, lens), lambda: cache.attention(1, q, table, lens.cpu()),
+           lambda: cache.attention(1, q, table, lens, out=t.zeros(2, 4, 64, device="cuda")),
+           lambda: cache.store(1, k, k[:1], table, lens), lambda: cache.store(1, k, k.half(), table, lens),
+           lambda: cache.store(1, k[:, :1], k[:, :1], table, lens), lambda: cache.store(-1, k, k, table, lens),
+           lambda: cache.store(1, k[:1], k[:1], table, lens),
+           lambda: cache.store(1, t.zeros(2, 2, 66, device="cuda")[:, :, 1:65], k, table, lens),
+           lambda: prb.KV8Cache(cache.k, cache.v, cache.k_scale[:, :, :, :1], cache.v_scale),
+           lambda: prb.KV8Cache(cache.k.float(), cache.v, cache.k_scale, cache.v_scale),
+           lambda: prb.KV8Cache(cache.k, cache.v[:2], cache.k_scale, cache.v_scale),
+           lambda: prb.KV8Cache.empty(4, 1, 2, 96), lambda: prb.KV8Cache.empty(4, 1, 2, 64, 64, 48)]
+    for i, call in enumerate(bad):
+        with pytest.raises(prb.MkError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    cache.check()
+
+
 def test_device_checks_make_the_sequence_nan():
     import persistent_runtime_b200 as prb
     t = torch()
@@ -213,3 +244,40 @@ def test_streams_graphs_and_two_calls_at_once():
         for (g, out), w in zip(graphs, want):
             assert t.equal(out, w)
     cache.check()
+
+
+def test_offsets_beyond_32_bits():
+    """The last pages of pools of more than 2^32 codes: store, attention and page copies."""
+    import persistent_runtime_b200 as prb
+    t = torch()
+    P, T, layers, H, D = 64, 64, 36, 8, 128
+    n_pages = (1 << 32) // (layers * H * P * D) + 40
+    if t.cuda.mem_get_info()[0] < 2 * n_pages * layers * H * P * D + (1 << 30):
+        pytest.skip("not enough free device memory")
+    cache = prb.KV8Cache.empty(n_pages, layers, H, D, P, T)
+    lens, new = np.array([100, 30]), np.array([3, 1])
+    pages = np.arange(n_pages - 3, n_pages, dtype=np.int32)
+    assert (int(pages[0]) * layers + 35) * H * P * D > 1 << 32
+    table = np.array([[pages[1], pages[2], -1], [pages[0], -1, -1]], np.int32)
+    small = ref.Cache(3, 1, H, D, P, T, "int8", 20)  # the same pages as 0, 1, 2 of a small host cache
+    for x, y in zip((cache.k, cache.v), small.codes):
+        x[n_pages - 3:, 35] = t.from_numpy(y[:, 0].view(np.int8)).cuda()
+    for x, y in zip((cache.k_scale, cache.v_scale), small.scales):
+        x[n_pages - 3:, 35] = t.from_numpy(y[:, 0]).cuda()
+    start = np.array([0, 3, 4], np.int32)
+    rng = np.random.default_rng(21)
+    k, v = (rng.standard_normal((4, H, D)).astype(np.float32) for _ in range(2))
+    q = t.from_numpy(rng.standard_normal((4, 32, D)).astype(np.float32))
+    d_len = dev(lens.astype(np.int32))
+    cache.store(35, dev(k), dev(v), dev(table), d_len, row_start=dev(start))
+    out, lse = cache.attention(35, q.cuda(), dev(table), d_len, row_start=dev(start), max_rows=3, return_lse=True)
+    cache.check()
+    small_table = [[1, 2], [0]]
+    small.store(0, [k, v], small_table, lens.tolist(), start)
+    check(out, lse, small, 0, q, np.array([[1, 2], [0, 0]]), lens, start, D ** -0.5, "float32")
+    for x, y in zip((cache.k, cache.v), small.codes):
+        np.testing.assert_array_equal(x[n_pages - 3:, 35].cpu().numpy().view(np.uint8), y[:, 0])
+    held = prb.PagePool(dev(table), t.zeros(n_pages, dtype=t.int32, device="cuda"), P, cache.pools())
+    held.copy(dev(pages[:1]), dev(np.array([5], np.int32)))
+    held.check()
+    assert t.equal(cache.k[5, 35], cache.k[n_pages - 3, 35]) and t.equal(cache.v_scale[5, 35], cache.v_scale[n_pages - 3, 35])

@@ -257,3 +257,23 @@ def test_captured_calls_and_another_stream():
     pages.free(gone, stream=st)
     pages.compact(stream=st)
     same(host, pages)
+
+
+def test_the_binding_refuses():
+    import persistent_runtime_b200 as prb
+    t = torch()
+    host = Host(4, 3, 16, 8)
+    pages = host.device()
+    table, counts, pool = pages.page_table, pages.ref_count, pages.pools[0]
+    bad = [lambda: pages.fork(i32([0]), i32([1, 2])), lambda: pages.fork(i32([0]).long(), i32([1])),
+           lambda: pages.free(i32([0]).cpu()), lambda: pages.reserve(i32([0]), i32([1, 1, 1, 1])),
+           lambda: pages.copy(i32([0, 1, 2, 3])[::2], i32([4, 5])),
+           lambda: prb.PagePool(table, counts, 16, [pool[:7]]), lambda: prb.PagePool(table, counts, 0, [pool]),
+           lambda: prb.PagePool(table, counts.float(), 16, [pool]), lambda: prb.PagePool(table[0], counts, 16, [pool]),
+           lambda: prb.PagePool(table, counts, 16, [pool] * 9), lambda: prb.PagePool(table, counts, 16, [pool.t()]),
+           lambda: prb.PagePool(table, counts, 16, [t.zeros(8, 3, dtype=t.int8, device="cuda")])]
+    for i, call in enumerate(bad):
+        with pytest.raises(prb.MkError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    same(host, pages)
