@@ -1017,7 +1017,7 @@ AttnPlan plan_of(const mk_kv8_cache &c, const mk_batch &b, int n_q_heads, int dt
     p.warps = pairs <= sms ? 8 : 4;
     return p;
   }
-  p.warps = p.mode == kRows8F32 ? 4 : 8;
+  p.warps = p.mode == kRows8F32 || pairs > sms ? 4 : 8;
   p.ctas = (int)std::min<int64_t>((int64_t)sms * ctas_per_sm(p.warps), (pairs * chunks + kMinUnits - 1) / kMinUnits);
   p.bytes = (int64_t)p.ctas * (32 + 2 * rg * 8 + 2ll * rg * c.head_dim * 4);
   return p;
