@@ -27,7 +27,7 @@ def nvcc() -> str:
 def build(verbose: bool = False, extra: list | None = None) -> str:
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
     cmd = [nvcc(), *ARCH, "-lineinfo", "-O3", "-std=c++17", "--expt-relaxed-constexpr",
-           "-Xcompiler", "-fPIC,-O2", "-shared", "-I", os.path.join(ROOT, "include"),
+           "-Xcompiler", "-fPIC,-O2", "-shared", "--threads", "0", "-I", os.path.join(ROOT, "include"),
            "-I", CSRC, *srcs, "-o", LIB, "-lcudart", *(extra or [])]
     if verbose:
         print(" ".join(cmd))
