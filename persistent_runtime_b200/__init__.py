@@ -623,8 +623,10 @@ class KV8Cache(_Status):
                 ws.data_ptr() if size else None, size, self._stream(stream))
             if rc:
                 _check(rc)
-            if ws is not None and stream is not None:
-                ws.record_stream(stream)
+            if stream is not None:  # the new tensors are the current stream's
+                for t in (ws, out, lse):
+                    if t is not None:
+                        t.record_stream(stream)
         return (out, lse) if return_lse else out
 
 

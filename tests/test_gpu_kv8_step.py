@@ -261,3 +261,47 @@ def test_the_step_in_a_graph():
     for x, y in zip(cache.pools(), cache2.pools()):
         assert t.equal(x, y)
     mk.close()
+
+
+FIRST_CALLS = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import numpy as np, torch
+import kv8_ref as ref, persistent_runtime_b200 as prb
+from kv8_ref import dev
+table, n = ref.make_table([3000, 2500], 64)
+cache = ref.Cache(n, 1, 8, 128, 64, 64, "int8", 1).device()
+q = torch.randn(2, 32, 128, device="cuda", dtype=torch.bfloat16)
+k = torch.randn(2, 8, 128, device="cuda")
+lens, table = dev(np.array([2990, 2400], np.int32)), dev(table)
+held = prb.PagePool.empty(4, 10, 64, cache.pools())
+a, b, c = (dev(np.array([x], np.int32)) for x in (0, 1, 3))
+six = c + 3
+zero, one = dev(np.zeros(4, np.int32)), dev(np.array([1, 0, 1, 0], np.int32))
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    held.reserve(zero, one)
+    held.fork(a, b)
+    held.free(a)
+    held.compact()
+    held.copy(c, six)
+    cache.store(0, k, k, table, lens)
+    out = cache.attention(0, q, table, lens)
+g.replay()
+cache.check()
+held.check()
+assert torch.equal(out, cache.attention(0, q, table, lens))
+assert held.page_table[:, 0].tolist() == [-1, 0, 1, -1], held.page_table
+print("ok")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALLS.format(root=os.path.dirname(tests), tests=tests)
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and done.stdout.strip() == "ok", done.stderr[-2000:]
