@@ -837,8 +837,8 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm(W)) kv8_attention_kernel(c
     if (g < y.groups) run_segment<D, FMT, MODE, W>(a, smem, q, hk, g, 0, y.chunks, true, 0);
     return;
   }
-  // The line: every warp adds up all sequences, 32 at a time, and finds the one
-  // in which the CTA's piece begins.
+  // The line: the units of all sequences, and, 32 at a time by every warp, the
+  // sequence in which the CTA's piece begins.
   const int lane = threadIdx.x & 31;
   SeqRows mine;   // sequence s0 + lane
   SeqLine line;
@@ -862,12 +862,40 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm(W)) kv8_attention_kernel(c
     }
   };
   int total = 0, pairs = 0, longest = 0;
-  for (int first = 0; first < a.b.n_seqs; first += 32) {
-    group(first);
-    if (mine.bad && threadIdx.x < 32 && mine.s % (int)gridDim.x == (int)blockIdx.x) reject(a, mine);
-    total += __shfl_sync(0xffffffffu, upto, 31);
-    pairs += __reduce_add_sync(0xffffffffu, line.groups * a.c.n_kv_heads);
-    longest = max(longest, __reduce_max_sync(0xffffffffu, line.chunks));
+  auto count = [&](const SeqRows &q, const SeqLine &y, bool reports) {
+    if (q.bad && reports && q.s % (int)gridDim.x == (int)blockIdx.x) reject(a, q);
+    total += y.units;
+    pairs += y.groups * a.c.n_kv_heads;
+    longest = max(longest, y.chunks);
+  };
+  if (a.b.n_seqs <= 32) {
+    group(0);
+    count(mine, line, threadIdx.x < 32);
+  } else {  // the warps share the sequences
+#pragma unroll 4
+    for (int s = threadIdx.x; s < a.b.n_seqs; s += W * 32) {
+      const SeqRows q = seq_rows(a.b, a.c.page_size, s);
+      count(q, seq_line<MODE>(a, q), true);
+    }
+  }
+  total = __reduce_add_sync(0xffffffffu, total);
+  pairs = __reduce_add_sync(0xffffffffu, pairs);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (a.b.n_seqs > 32) {
+    __shared__ int sums[3][W];
+    if (lane == 0) {
+      sums[0][threadIdx.x >> 5] = total;
+      sums[1][threadIdx.x >> 5] = pairs;
+      sums[2][threadIdx.x >> 5] = longest;
+    }
+    __syncthreads();
+    total = pairs = longest = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      total += sums[0][w];
+      pairs += sums[1][w];
+      longest = max(longest, sums[2][w]);
+    }
   }
   // the host allows fewer than 2^30 units
   const int per = max(kMinUnits, a.by_grid.quotient(total + (int)gridDim.x - 1));
