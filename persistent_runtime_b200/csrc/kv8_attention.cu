@@ -112,12 +112,13 @@ struct AttnArgs {
 
 constexpr int group_rows(int mode) { return mode == kRows16 ? 16 : 8; }
 
-// A CTA has 8 warps and an SM to itself, or 4 warps and half of one; their
-// registers allow no more.  Cut lines: 8 (one long sequence of e4m3 56 us against
-// 59), with fp32 rows 4 (batch 8 22.5 against 26).  Whole pairs: 8 while every
-// pair has an SM to itself (one sequence of 250: 6.2 us against 8), else 4, whose
-// fixed costs overlap (64 sequences of 250: 16 us against 20.6).
-__host__ __device__ constexpr int ctas_per_sm(int warps) { return warps == 4 ? 2 : 1; }
+// A CTA has 8 warps and an SM to itself, 4 warps and half of one, or 2 and a
+// quarter: the registers of 8 warps are an SM's.  Few pairs: 8 (one long sequence
+// of e4m3 53 us against 59 with 4), with fp32 rows and cut lines 4 (batch 8 22.5
+// against 26 at that time).  More pairs than SMs: 4, more than twice as many: 2,
+// because what a pair costs besides its chunks then overlaps with other pairs' (64
+// sequences of 250: 20.6, 13.2 and 11.0 us with 8, 4 and 2).
+__host__ __device__ constexpr int ctas_per_sm(int warps) { return 8 / warps; }
 
 // What a pair costs a CTA besides its chunks (query rows, the warps' results),
 // in units of a chunk.
@@ -224,6 +225,12 @@ __device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp; results below 2
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// x 2^e, for |e| up to 250: in two factors that are normal numbers.
+__device__ __forceinline__ float times_pow2(float x, int e) {
+  const int h = e >> 1;
+  return x * __uint_as_float((uint32_t)(127 + h) << 23) * __uint_as_float((uint32_t)(127 + e - h) << 23);
 }
 
 // Codes to fp16 pairs, exactly: word w (4 e4m3 codes) -> (code 0, code 1), (code 2, code 3).
@@ -490,12 +497,25 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
     const int col = warp + n * W;
     if (RG % W != 0 && col >= RG) break;
     const float(&x)[D / 32] = x_row[n];
+    if (lim_row[n] == 0) {  // no such row: its column adds nothing and is not read
+#pragma unroll
+      for (int u = 0; u < NQ; ++u) {
+        if constexpr (INT && D == 64) *reinterpret_cast<uint16_t *>(qs + u * RG * D + col * D + lane * 2) = 0;
+        else if constexpr (INT || D == 64) *reinterpret_cast<uint32_t *>(qs + (u * RG * D + col * D) * QB + lane * 4) = 0;
+        else *reinterpret_cast<uint2 *>(qs + (u * RG * D + col * D) * QB + lane * 8) = make_uint2(0, 0);
+      }
+      if (lane == 0) {
+        sh_f[col] = 0.0f;
+        sh_limit[col] = 0;
+      }
+      continue;
+    }
     uint32_t top = 0;  // bits of the largest magnitude: above those of infinity for a NaN
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) top = max(top, __float_as_uint(x[d]) & 0x7fffffffu);
     top = __reduce_max_sync(0xffffffffu, top);
     const int e = (int)(top >> 23) - 126;  // |q| < 2^e
-    const float shrink = ldexpf(1.0f, -e);
+    const float shrink = times_pow2(1.0f, -e);
     uint8_t *dst = qs + (col * D + lane * (D / 32)) * QB;
     constexpr float kOne = INT ? 127.0f * 16384.0f : 1.0f;
     if constexpr (INT) {
@@ -532,7 +552,7 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
     }
     if (lane == 0) {
       // integers have no NaN: the row's factor carries it
-      sh_f[col] = INT && top >= 0x7f800000u ? __int_as_float(0x7fc00000) : ldexpf(a.scale * kLog2e / kOne, e);
+      sh_f[col] = INT && top >= 0x7f800000u ? __int_as_float(0x7fc00000) : times_pow2(a.scale * (kLog2e / kOne), e);
       sh_limit[col] = lim_row[n];
     }
   }
@@ -1042,10 +1062,10 @@ AttnPlan plan_of(const mk_kv8_cache &c, const mk_batch &b, int n_q_heads, int dt
   const int sms = sm_count(c.device);
   if (p.pair_mode) {
     p.ctas = (int)pairs;
-    p.warps = pairs <= sms ? 8 : 4;
+    p.warps = pairs <= sms ? 8 : pairs <= 2 * sms ? 4 : 2;
     return p;
   }
-  p.warps = p.mode == kRows8F32 || pairs > sms ? 4 : 8;
+  p.warps = pairs > 2 * sms ? 2 : p.mode == kRows8F32 || pairs > sms ? 4 : 8;
   p.ctas = (int)std::min<int64_t>((int64_t)sms * ctas_per_sm(p.warps), (pairs * chunks + kMinUnits - 1) / kMinUnits);
   p.bytes = (int64_t)p.ctas * (32 + 2 * rg * 8 + 2ll * rg * c.head_dim * 4);
   return p;
@@ -1071,7 +1091,9 @@ cudaError_t launch(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
 
 template <int D, int FMT, int MODE>
 cudaError_t launch(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
-  return p.warps == 4 ? launch<D, FMT, MODE, 4>(a, p, st) : launch<D, FMT, MODE, 8>(a, p, st);
+  return p.warps == 2   ? launch<D, FMT, MODE, 2>(a, p, st)
+         : p.warps == 4 ? launch<D, FMT, MODE, 4>(a, p, st)
+                        : launch<D, FMT, MODE, 8>(a, p, st);
 }
 
 template <int D, int FMT>
