@@ -489,7 +489,8 @@ mk_status mk_kv8_attention_workspace(const mk_kv8_cache *cache, int n_q_heads, i
  * mk_kv8_attention.  The cache's layers, kv heads and head_dim must be the
  * handle's; d_page_table is int32 [batch][max_pages] with max_pages *
  * page_size >= kv_capacity; the handle may be built for contiguous or paged
- * K/V.  Tokens, lengths, logits and device-side errors (in the handle's
+ * K/V.  A page that holds a sequence's new position must be its own
+ * (mk_pages_reserve).  Tokens, lengths, logits and device-side errors (in the handle's
  * status word) are those of mk_decode_step; additionally a page table entry
  * out of range under a position of the step makes the step write nothing.
  * Workspace: mk_decode_step_kv8_workspace bytes, 16-byte aligned, not to be
@@ -559,7 +560,8 @@ mk_status mk_pages_reserve(const mk_pages *pages, const int32_t *d_kv_len, const
 /*
  * mk_pages_compact - move the U pages in use to the page numbers 0 .. U - 1:
  * the i-th page in use with a number >= U moves to the i-th free number < U.
- * Contents, counts and every table entry follow.  Device check: MK_CHECK_PAGE
+ * Contents, counts and every table entry follow (a page that is counted although
+ * no entry names it moves like the others).  Device check: MK_CHECK_PAGE
  * (an entry outside [-1, n_pages), or one that names a free page: the call
  * then changes nothing).
  */

@@ -541,14 +541,17 @@ class KV8Cache(_Status):
         """Fills argument structure `slot` with the rows x; returns their number."""
         shape, stride = x.shape, x.stride()
         if len(shape) != 3 or (n_heads and shape[1] != n_heads) or shape[2] != self.head_dim \
-                or stride[2] != 1:
+                or (stride[2] != 1 and shape[0]):
             _refuse(f"{what} must be [rows][{n_heads or 'heads'}][{self.head_dim}] with contiguous "
                     "head_dim")
         dtype = self._dtypes.get(x.dtype)
         if dtype is None or x.get_device() != self._index:
             _refuse(f"{what} must be float32, bfloat16 or float16 on {self.device}")
         r = self._args[slot]
-        r.data, r.dtype, r.row_stride, r.head_stride = x.data_ptr(), dtype, stride[0], stride[1]
+        r.data, r.dtype = x.data_ptr(), dtype
+        # the stride of a single row or head is never used, and may be anything
+        r.row_stride = stride[0] if shape[0] > 1 else 0
+        r.head_stride = stride[1] if shape[1] > 1 else 0
         return shape[0]
 
     def _fill_batch(self, start, n_seqs, n_rows, max_rows, max_pages, kv_len, page_table):

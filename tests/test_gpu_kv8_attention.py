@@ -147,6 +147,25 @@ def test_strides_bounds_and_repeats():
         assert t.equal(cache.attention(1, q.cuda(), *args, row_start=dev(start), max_rows=3), want)
 
 
+def test_no_rows():
+    t = torch()
+    case = (4, 2, 64, 32, 16, "int8", "bfloat16", [40, 50], [0, 0])
+    host, q, table, cached, new, start = setup(case, 18)
+    cache = host.device()
+    args = (dev(table), dev(cached.astype(np.int32)))
+    out, lse = cache.attention(0, q.cuda(), *args, row_start=dev(start), max_rows=1, return_lse=True)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    cache.store(0, q[:, :2].cuda(), q[:, :2].cuda(), *args, row_start=dev(start))
+    # rows that belong to nobody, and a batch without any row in its sequences
+    two = t.ones(2, 4, 64, device="cuda", dtype=t.bfloat16)
+    out = t.full_like(two, 3.0)
+    cache.attention(0, two, *args, row_start=dev(start), max_rows=1, out=out)
+    before = [x.clone() for x in cache.pools()]
+    cache.store(0, two[:, :2], two[:, :2], *args, row_start=dev(start))
+    cache.check()
+    assert bool((out == 3).all()) and all(t.equal(x, y) for x, y in zip(cache.pools(), before))
+
+
 def test_the_binding_refuses():
     import persistent_runtime_b200 as prb
     t = torch()

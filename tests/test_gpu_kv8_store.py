@@ -133,6 +133,18 @@ def test_strided_rows_and_rows_behind_the_last_sequence():
     same(host, cache)
 
 
+def test_strides_of_a_single_row_or_head_may_be_anything():
+    t = torch()
+    table, n_pages = make_table([20], 32)
+    host = ref.Cache(n_pages, 1, 1, 64, 32, 16, "int8", 1)
+    cache = host.device()
+    x = t.randn(1, 1, 64, device="cuda").as_strided((1, 1, 64), (3, 5, 1))
+    cache.store(0, x, x, dev(table), dev(np.array([10], np.int32)))
+    cache.check()
+    host.store(0, [x.cpu().numpy()] * 2, table, [10], [0, 1])
+    same(host, cache)
+
+
 def test_device_checks_leave_out_what_is_wrong():
     import persistent_runtime_b200 as prb
     table, n_pages = make_table([40, 40, 40], 32, extra=0)

@@ -277,3 +277,51 @@ def test_the_binding_refuses():
             call()
             pytest.fail(f"call {i} was not refused")
     same(host, pages)
+
+
+@pytest.mark.usefixtures("built_libs")
+def test_the_paged_step_on_shared_pages():
+    """Sequences forked between steps of mk_decode_steps_paged: bitwise the contiguous step on
+    caches that are copied."""
+    import persistent_runtime_b200 as prb
+    import synth
+    from gpu_helpers import dev_weights
+    t = torch()
+    B, P, cap = 3, 64, 200
+    w = synth.TINY.with_(name="tiny-b3", batch=B, kv_len=0, steps=1)
+    weights = dev_weights(synth.make_weights(w, 8))
+    flat, paged = prb.Megakernel(w, cap, 0), prb.Megakernel(w, cap, 0, kv_page_size=P)
+    flat.load_weights(weights)
+    paged.load_weights(weights)
+    k, v = (t.zeros(w.n_layers, B, w.n_kv_heads, cap, w.head_dim, dtype=t.int16, device="cuda") for _ in range(2))
+    pools = [t.zeros(10, w.n_layers, w.n_kv_heads, P, w.head_dim, dtype=t.int16, device="cuda") for _ in range(2)]
+    pages = prb.PagePool.empty(B, -(-cap // P), P, pools)
+    ones = i32([1] * B)
+    tok_f, len_f, out_f = i32([5, 9, 11]), i32([0, 0, 0]), t.zeros(B, w.vocab, device="cuda")
+    tok_p, len_p, out_p = tok_f.clone(), len_f.clone(), out_f.clone()
+
+    def steps(n):
+        for _ in range(n):
+            pages.reserve(len_p, ones)
+            paged.decode_steps_paged(1, tok_p, tok_p, len_p, *pools, 10, pages.page_table, out_p)
+            flat.decode_step(tok_f, tok_f, len_f, k, v, out_f)
+            assert t.equal(tok_f, tok_p) and t.equal(out_f, out_p) and t.equal(len_f, len_p)
+        assert paged.sync_status()[0] == 0 and flat.sync_status()[0] == 0
+        pages.check()
+
+    steps(70)
+    for a, b in ((0, 2), (2, 1)):  # one continued as two, then again
+        pages.free(i32([b]))
+        pages.fork(i32([a]), i32([b]))
+        for x in (k, v):
+            x[:, b] = x[:, a]
+        for length in (len_f, len_p):
+            length[b] = length[a]
+        for tok in (tok_f, tok_p):
+            tok[b] = (int(tok[a]) + 1) % w.vocab
+        steps(3)
+        assert int(pages.ref_count.max()) > 1
+        pages.compact()
+        steps(30)
+    flat.close()
+    paged.close()
