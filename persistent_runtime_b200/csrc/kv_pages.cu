@@ -351,8 +351,10 @@ __global__ void __launch_bounds__(kTeamThreads) reserve_kernel(const __grid_cons
   int at = t.scan(need, all_need);
   int k = t.scan(n_free, all_free);
   if (all_free < all_need) {
-    if (t.index() == 0)
+    if (t.index() == 0) {
+      a.head->copies = 0;  // room was given out, but nothing is listed
       record_status(a.p.d_status, MK_ERR_OOM, a.p.n_pages, all_need - all_free, MK_CHECK_FREE);
+    }
     return;
   }
   if (all_need == 0) return;

@@ -215,6 +215,43 @@ def test_failures_change_nothing():
     assert pages.sync_status()[1][3] == 3
 
 
+@pytest.mark.parametrize("n_pages", [9, 4200])  # one CTA, two
+def test_reserve_without_room_for_shared_pages(n_pages):
+    """Too few free pages while several sequences write shared pages: nothing is copied, whatever an earlier call
+    has left in the workspace."""
+    import persistent_runtime_b200 as prb
+
+    host = Host(7, n_pages, 16, 9)
+    host.n_pages, host.ref = n_pages, np.zeros(n_pages, np.int32)
+    host.pools = [np.arange(n_pages * w, dtype=np.int32).reshape(n_pages, w) for w in (4, 1027)]
+    used = n_pages - 4
+    host.hold(0, [0, 1, 2])
+    host.hold(1, [3])
+    host.hold(6, range(4, used))
+    pages = host.device()
+    fork = [0, 0, 1], [2, 3, 4]
+    pages.fork(*map(i32, fork))
+    host.fork(*fork)
+    lens, new = [40, 5, 40, 40, 5, 0, 0], [1, 0, 1, 0, 1, 0, 0]
+    pages.reserve(i32(lens), i32(new))  # three copies, listed in the workspace
+    host.reserve(lens, new)
+    same(host, pages)
+    for pool, dev_pool in zip(host.pools, pages.pools):  # a repeated copy would show
+        pool += 1
+        dev_pool += 1
+    fork = [0, 1], [2, 4]
+    pages.free(i32([2, 4]))
+    host.free([2, 4])
+    pages.fork(*map(i32, fork))
+    host.fork(*fork)
+    for lens, new in (([3, 3, 3, 3, 3, 0, 0], [1, 1, 1, 1, 1, 64, 0]), ([0] * 7, [48, 16, 48, 48, 16, 64, 16])):
+        pages.reserve(i32(lens), i32(new))
+        rc, d = pages.sync_status()
+        assert rc == prb.MK_ERR_OOM and d[3] == 6
+        pages.reset()
+        same(host, pages)
+
+
 def test_captured_calls_and_another_stream():
     t = torch()
     host = Host(6, 4, 16, 30)
