@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(256) kv8_store_kernel(const __grid_constant__ 
   const int s = a.b.d_row_start ? find_seq(a.b, a.t_log2, slot) : slot;  // without: one block per sequence
   const SeqRows q = seq_rows(a.b, P, s);
   const int i = a.b.d_row_start ? (int)(slot - ((q.r0 >> a.t_log2) + 2ll * s)) : 0;
-  if (q.bad || q.n == 0 || i < 0) return;
+  // slots behind the blocks of a sequence: rows behind the last one, or a row_start out of order
+  if (q.bad || q.n == 0 || i < 0 || i > (q.n >> a.t_log2) + 1) return;
   const int first = ((q.c >> a.t_log2) + i) << a.t_log2;  // first position of the block
   const int end = q.c + q.n;
   if (first >= end) return;

@@ -133,6 +133,23 @@ def test_strided_rows_and_rows_behind_the_last_sequence():
     same(host, cache)
 
 
+def test_a_billion_rows_behind_the_last_sequence():
+    """Positions and rows near 2^30 and 2^31: slots that belong to no block do nothing."""
+    t = torch()
+    n, c, P = (1 << 30) + 1024, (1 << 31) - (1 << 20), 128
+    host = ref.Cache(1, 1, 1, 64, P, 128, "int8", 1)
+    cache, want = host.device(), host.device()
+    x = t.randn(1, 1, 64, device="cuda")
+    table = t.full((1, c // P + 1), -1, dtype=t.int32, device="cuda")
+    table[0, c // P] = 0
+    rows = x.expand(n, 1, 64)
+    cache.store(0, rows, rows, table, dev(np.array([c], np.int32)), row_start=dev(np.array([0, 1], np.int32)))
+    cache.check()
+    want.store(0, x, x, dev(np.zeros((1, 1), np.int32)), dev(np.zeros(1, np.int32)))
+    for a, b in zip(cache.pools(), want.pools()):
+        assert t.equal(a, b)
+
+
 def test_strides_of_a_single_row_or_head_may_be_anything():
     t = torch()
     table, n_pages = make_table([20], 32)
