@@ -564,13 +564,16 @@ const char *check_pages(const mk_pages *p) {
   if ((int64_t)p->n_seqs * p->max_pages >= (1ll << 31) || (int64_t)p->max_pages * p->page_size >= (1ll << 31))
     return "page tables of 2^31 entries or positions and more are not supported";
   if (p->n_pools < 0 || p->n_pools > MK_MAX_POOLS) return "n_pools must be 0 .. MK_MAX_POOLS";
-  int64_t bytes = 0;
+  int64_t bytes = 0, steps = 0;  // steps of the copy of one page
   for (int i = 0; i < p->n_pools; ++i) {
     if (!p->d_pool[i] || (reinterpret_cast<uintptr_t>(p->d_pool[i]) & 3)) return "a pool is null or not 4-byte aligned";
     if (p->page_bytes[i] < 4 || (p->page_bytes[i] & 3)) return "page_bytes must be a positive multiple of 4";
     bytes += p->page_bytes[i];
+    steps += (p->page_bytes[i] + kCopyBytes - 1) / kCopyBytes;
   }
   if (bytes >= (1ll << 40)) return "page_bytes out of range";
+  // they are counted in 32 bits; the margin is what the CTAs count beyond the last
+  if (steps * p->n_pages >= (1ll << 31) - (1 << 20)) return "pools of 2^31 pages and more are not supported";
   if (!p->d_page_table || !p->d_ref) return "null page table or counts";
   return nullptr;
 }

@@ -181,3 +181,14 @@ def test_binding_structures_match_the_header_layouts(tmp_path):
     for (name, kind), value in got.items():
         if kind == "value":
             assert getattr(prb, name) == value, name
+
+
+def test_page_calls_refuse_more_pages_than_a_copy_counts():
+    many = pages(n_pages=1 << 29, n_pools=4)
+    for i in range(4):
+        many.d_pool[i], many.page_bytes[i] = A, 4
+    size = ctypes.c_int64()
+    refused(prb.lib().mk_pages_workspace(ctypes.byref(many), 0, ctypes.byref(size)), "2^31 pages")
+    refused(prb.lib().mk_pages_compact(ctypes.byref(many), A, 1 << 40, None), "2^31 pages")
+    many.n_pages = 1 << 28
+    assert prb.lib().mk_pages_workspace(ctypes.byref(many), 0, ctypes.byref(size)) == prb.MK_OK
