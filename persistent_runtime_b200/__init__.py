@@ -369,12 +369,13 @@ class Megakernel:
         max_pages = page_table.shape[1]
         _check(lib().mk_decode_step_kv8_workspace(self._h, cache._ref, max_pages,
                                                   ctypes.byref(size)), self._h)
-        ws = torch.empty(size.value, dtype=torch.uint8, device=cache.device)
+        if stream is None:
+            stream = torch.cuda.current_stream(cache.device)
+        with cache._given(stream):
+            ws = torch.empty(size.value, dtype=torch.uint8, device=cache.device)
         _check(lib().mk_decode_step_kv8(self._h, _ptr(tokens_in), _ptr(tokens_out), _ptr(kv_len),
                                         cache._ref, page_table.data_ptr(), max_pages, _ptr(logits),
                                         ws.data_ptr(), size.value, _stream_ptr(stream)), self._h)
-        if stream is not None:
-            ws.record_stream(stream)
 
     def sync_status(self, stream=None):
         """Returns (status, detail[4]); status 0 = ok."""
@@ -457,6 +458,14 @@ class _Status:
     def _stream(self, stream):
         """The raw stream: the given one, or the device's current one."""
         return self._raw_stream(self._index) if stream is None else stream.cuda_stream
+
+    def _given(self, stream):
+        """A context in which `stream` is the current one: what a call allocates for itself must
+        be free on the stream that uses it, not only on the one that is current."""
+        import torch
+        if stream.device_index != self._index:
+            _refuse(f"the stream is not one of {self.device}")
+        return torch.cuda.stream(stream)
 
     def _bind(self, device):
         import torch
@@ -594,6 +603,17 @@ class KV8Cache(_Status):
         positions 0 to kv_len[s] + i.  max_rows bounds the rows of one sequence (1 without
         row_start; at most MK_KV8_MAX_ROWS).  Returns the output in q's type, and with
         return_lse also the float32 log-sum-exp [n_rows][n_q_heads]."""
+        if stream is not None:
+            import torch
+            now = torch.cuda.current_stream(self.device)
+            with self._given(stream):
+                got = self.attention(layer, q, page_table, kv_len, row_start, max_rows, scale, out,
+                                     return_lse)
+            # both streams may still use what is returned when the caller drops it
+            for t in got if return_lse else (got,):
+                t.record_stream(stream)
+                t.record_stream(now)
+            return got
         n_rows = self._rows(0, q, 0, "q")
         n_heads = q.shape[1]
         if max_rows is None:
@@ -623,13 +643,9 @@ class KV8Cache(_Status):
             rc = self._lib.mk_kv8_attention(
                 self._ref, layer, rq, n_heads, self.head_dim ** -0.5 if scale is None else scale,
                 out.data_ptr(), lse.data_ptr() if return_lse else None, b,
-                ws.data_ptr() if size else None, size, self._stream(stream))
+                ws.data_ptr() if size else None, size, self._stream(None))
             if rc:
                 _check(rc)
-            if stream is not None:  # the new tensors are the current stream's
-                for t in (ws, out, lse):
-                    if t is not None:
-                        t.record_stream(stream)
         return (out, lse) if return_lse else out
 
 
@@ -686,13 +702,14 @@ class PagePool(_Status):
         return size
 
     def _call(self, fn, n, args, stream):
+        if stream is not None:
+            with self._given(stream):
+                return self._call(fn, n, args, None)
         size = self._workspace(n)
         ws = self._bytes(size)
-        rc = fn(self._ref, *args, ws.data_ptr(), size, self._stream(stream))
+        rc = fn(self._ref, *args, ws.data_ptr(), size, self._stream(None))
         if rc:
             _check(rc)
-        if stream is not None:
-            ws.record_stream(stream)
 
     def fork(self, src, dst, stream=None):
         """mk_pages_fork: sequences dst take (and share) the pages of sequences src."""

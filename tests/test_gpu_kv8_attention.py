@@ -300,3 +300,33 @@ def test_offsets_beyond_32_bits():
     held.copy(dev(pages[:1]), dev(np.array([5], np.int32)))
     held.check()
     assert t.equal(cache.k[5, 35], cache.k[n_pages - 3, 35]) and t.equal(cache.v_scale[5, 35], cache.v_scale[n_pages - 3, 35])
+
+
+def test_a_given_stream_gets_memory_of_its_own():
+    """What a call allocates must not be memory that was freed on the current stream, whose work may
+    still be using it."""
+    t = torch()
+    case = (16, 8, 128, 64, 64, "int8", "bfloat16", [3000, 2500], [1, 1])
+    host, q, table, cached, new, start = setup(case, 19)
+    cache = host.device()
+    args = 1, q.cuda(), dev(table), dev(cached.astype(np.int32))
+    made, make = [], cache._bytes
+
+    def spy(n):
+        made.append(make(n))
+        return made[-1]
+
+    cache._bytes = spy
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    first = cache.attention(*args, return_lse=True)
+    freed = {x.data_ptr() for x in (*first, *made)}
+    want = [x.clone() for x in first]
+    assert len(made) == 1
+    del first
+    made.clear()
+    got = cache.attention(*args, return_lse=True, stream=side)
+    assert len(made) == 1 and not freed & {x.data_ptr() for x in (*got, *made)}
+    t.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert t.equal(a, b)

@@ -362,3 +362,27 @@ def test_the_paged_step_on_shared_pages():
         steps(30)
     flat.close()
     paged.close()
+
+
+def test_a_given_stream_gets_a_workspace_of_its_own():
+    t = torch()
+    host = Host(3, 4, 16, 8)
+    host.hold(0, [5, 2])
+    pages = host.device()
+    made, make = [], pages._bytes
+
+    def spy(n):
+        made.append(make(n))
+        return made[-1]
+
+    pages._bytes = spy
+    side = t.cuda.Stream()
+    pages.fork(i32([0]), i32([1]))
+    host.fork([0], [1])
+    freed = made.pop().data_ptr()
+    src, dst = i32([0]), i32([2])
+    t.cuda.synchronize()
+    pages.fork(src, dst, stream=side)
+    host.fork([0], [2])
+    assert made.pop().data_ptr() != freed
+    same(host, pages)
