@@ -505,7 +505,9 @@ mk_status mk_decode_step_kv8_workspace(mk_handle *h, const mk_kv8_cache *cache, 
 
 /* Pools of pages (of bf16 or 8-bit caches) and who holds which page.  ref[p]
  * counts the page table entries that name page p; a page with 0 is free.  A
- * caller begins with every table entry -1 (no page) and every count 0. */
+ * caller begins with every table entry -1 (no page) and every count 0.
+ * Refused: tables of 2^31 entries, sequences of 2^31 positions, pools of 2^31
+ * pages (of all pools together; pages above 16 KB count once for every 16 KB). */
 enum { MK_MAX_POOLS = 8 };
 typedef struct {
   int device;
