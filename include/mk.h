@@ -463,7 +463,8 @@ mk_status mk_kv8_store(const mk_kv8_cache *cache, int layer, const mk_rows *k, c
  * enters with an error of at most 2^-21 of its row's largest (int8) or 2^-12
  * of itself (e4m3; fp32 rows 2^-23), a probability with 2^-17 of the largest of
  * its chunk of 32 positions (int8; fp32 rows 2^-24) or 2^-12 of itself (e4m3;
- * fp32 rows 2^-22).  max_rows is at most
+ * fp32 rows 2^-22; very small ones instead with 2^-24 of the row's largest
+ * element and 2^-39 of the chunk's largest probability).  max_rows is at most
  * MK_KV8_MAX_ROWS: the call is made for decoding, not for prompts.
  * Workspace: at least mk_kv8_attention_workspace bytes, 16-byte aligned; its
  * contents need not be initialised.  Results do not depend on how the work is

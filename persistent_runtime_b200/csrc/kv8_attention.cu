@@ -819,14 +819,26 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
   __syncthreads();  // before the next segment's copies and flags
 }
 
-// NaN for the rows of a sequence that failed a check, by one thread.
+// NaN for the rows of a sequence that failed a check, by a warp (there may be
+// many: max_rows need not bound them).
 __device__ __noinline__ void reject(const AttnArgs &a, const SeqRows &q) {
-  record_status(a.c.d_status, MK_ERR_DEVICE, q.s, q.value(a.b), q.bad);
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) record_status(a.c.d_status, MK_ERR_DEVICE, q.s, q.value(a.b), q.bad);
   const int64_t r0 = (int64_t)q.r0 * a.n_q_heads, n = (int64_t)q.n * a.n_q_heads;
   const float nan = __int_as_float(0x7fc00000);
-  for (int64_t i = 0; i < n * a.c.head_dim; ++i) store_out(a.out, a.q.dtype, r0 * a.c.head_dim + i, nan);
+  for (int64_t i = lane; i < n * a.c.head_dim; i += 32) store_out(a.out, a.q.dtype, r0 * a.c.head_dim + i, nan);
   if (a.lse)
-    for (int64_t i = 0; i < n; ++i) a.lse[r0 + i] = nan;
+    for (int64_t i = lane; i < n; i += 32) a.lse[r0 + i] = nan;
+}
+// The same for every such sequence that falls to this CTA, by its warps.
+template <int W>
+__device__ __noinline__ void reject_all(const AttnArgs &a) {
+  for (int first = (threadIdx.x >> 5) * 32; first < a.b.n_seqs; first += W * 32) {
+    const int s = first + (threadIdx.x & 31);
+    const bool mine = s < a.b.n_seqs && s % (int)gridDim.x == (int)blockIdx.x && seq_rows(a.b, a.c.page_size, s).bad;
+    for (uint32_t left = __ballot_sync(0xffffffffu, mine); left; left &= left - 1)
+      reject(a, seq_rows(a.b, a.c.page_size, first + __ffs(left) - 1));
+  }
 }
 
 // Units on the line of sequence s: for every pair its chunks, then
@@ -853,7 +865,7 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm(W)) kv8_attention_kernel(c
     const int hk = rest % a.c.n_kv_heads, s = rest / a.c.n_kv_heads;
     const SeqRows q = seq_rows(a.b, a.c.page_size, s);
     const SeqLine y = seq_line<MODE>(a, q);
-    if (q.bad && hk == 0 && g == 0 && threadIdx.x == 0) reject(a, q);
+    if (q.bad && hk == 0 && g == 0 && threadIdx.x < 32) reject(a, q);
     if (g < y.groups) run_segment<D, FMT, MODE, W>(a, smem, q, hk, g, 0, y.chunks, true, 0);
     return;
   }
@@ -881,23 +893,24 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm(W)) kv8_attention_kernel(c
       if (lane >= d) upto += v;
     }
   };
-  int total = 0, pairs = 0, longest = 0;
-  auto count = [&](const SeqRows &q, const SeqLine &y, bool reports) {
-    if (q.bad && reports && q.s % (int)gridDim.x == (int)blockIdx.x) reject(a, q);
+  int total = 0, pairs = 0, longest = 0, bad = 0;
+  auto count = [&](const SeqRows &q, const SeqLine &y) {
+    bad |= q.bad;
     total += y.units;
     pairs += y.groups * a.c.n_kv_heads;
     longest = max(longest, y.chunks);
   };
   if (a.b.n_seqs <= 32) {
     group(0);
-    count(mine, line, threadIdx.x < 32);
+    count(mine, line);
   } else {  // the warps share the sequences
 #pragma unroll 4
     for (int s = threadIdx.x; s < a.b.n_seqs; s += W * 32) {
       const SeqRows q = seq_rows(a.b, a.c.page_size, s);
-      count(q, seq_line<MODE>(a, q), true);
+      count(q, seq_line<MODE>(a, q));
     }
   }
+  if (__any_sync(0xffffffffu, bad)) reject_all<W>(a);
   total = __reduce_add_sync(0xffffffffu, total);
   pairs = __reduce_add_sync(0xffffffffu, pairs);
   longest = __reduce_max_sync(0xffffffffu, longest);

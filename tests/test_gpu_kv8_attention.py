@@ -330,3 +330,33 @@ def test_a_given_stream_gets_memory_of_its_own():
     t.cuda.synchronize()
     for a, b in zip(got, want):
         assert t.equal(a, b)
+
+
+@pytest.mark.parametrize("wide", [False, True])  # short tables (a CTA per pair), long ones
+def test_many_failing_sequences_and_rows(wide):
+    t = torch()
+    rng = np.random.default_rng(5)
+    n, bad = 200, [7, 40, 41, 199]
+    lens = rng.integers(0, 600, n)
+    new = np.ones(n, np.int64)
+    new[7] = 3000  # far above max_rows
+    new[150] = 2
+    case = (4, 2, 64, 64, 32, "int8", "bfloat16", list(lens), list(new))
+    case[7][7] = case[8][7] = 0  # the host's cache need not hold its rows
+    case[8][7] = 1
+    host, _, table, cached, _, _ = setup(case, 29)
+    start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = t.from_numpy(rng.standard_normal((start[-1], 4, 64)).astype(np.float32)).to(t.bfloat16)
+    given = cached.astype(np.int32)
+    given[bad[1:]] = -1
+    tab = np.full((n, 200), -1, np.int32) if wide else table
+    tab[:, :table.shape[1]] = table
+    cache = host.device()
+    out, lse = cache.attention(0, q.cuda(), dev(tab), dev(given), row_start=dev(start), max_rows=2, return_lse=True)
+    assert cache.sync_status()[1][1] in bad
+    owner = np.repeat(np.arange(n), new)
+    fails = t.from_numpy(np.isin(owner, bad)).cuda()
+    assert bool(t.isnan(out[fails]).all()) and bool(t.isnan(lse[fails]).all())
+    good = np.setdiff1d(np.arange(n), bad)
+    check(out[~fails], lse[~fails], host, 0, q[~fails.cpu()], table[good], cached[good],
+          np.concatenate([[0], np.cumsum(new[good])]), 64 ** -0.5, "bfloat16")
