@@ -120,6 +120,18 @@ constexpr int group_rows(int mode) { return mode == kRows16 ? 16 : 8; }
 // sequences of 250: 20.6, 13.2 and 11.0 us with 8, 4 and 2).
 __host__ __device__ constexpr int ctas_per_sm(int warps) { return 8 / warps; }
 
+// More pairs than four CTAs per SM: six CTAs of 2 warps, in 168 registers a thread,
+// where the code fits with few spills or none.  head_dim 64 (16 bf16 heads on 8,
+// int8): 96 sequences of 1000 36.6 -> 25.3 us, 112 to 512 of 250 12.6 -> 12.2 and 45.8
+// -> 37.1, 128 of up to 4000 68.6 -> 59.1.  head_dim 128 with 16-bit rows (32 heads on
+// 8): only for short page tables, 96 sequences of 250 17.7 -> 12.4 us, 512 65.0 -> 58.3
+// (128, which fill six CTAs just over once, 18.0 -> 18.9); long pairs run at the HBM
+// rate and would lose by the spills (96 of up to 4000 72.3 -> 75.5).
+constexpr int kCrowd = 6;
+__host__ __device__ constexpr bool crowd_fits(int D, int mode) {
+  return mode == kRows8 || (D == 64 && mode == kRows8F32);
+}
+
 // What a pair costs a CTA besides its chunks (query rows, the warps' results),
 // in units of a chunk.
 __host__ __device__ constexpr int pair_units(int mode) { return mode == kRows16 ? 16 : 8; }
@@ -854,8 +866,8 @@ __device__ __forceinline__ SeqLine seq_line(const AttnArgs &a, const SeqRows &q)
   return {chunks, groups, (chunks + pair_units(MODE)) * groups * a.c.n_kv_heads};
 }
 
-template <int D, int FMT, int MODE, int W>
-__global__ void __launch_bounds__(W * 32, ctas_per_sm(W)) kv8_attention_kernel(const __grid_constant__ AttnArgs a) {
+template <int D, int FMT, int MODE, int W, int CTAS>
+__global__ void __launch_bounds__(W * 32, CTAS) kv8_attention_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_trigger();  // the launch behind this one may get ready; it waits for this grid's end
   pdl_wait();
@@ -1058,7 +1070,7 @@ int mode_of(int dtype, int rep, int max_rows) {
 
 // Grid and workspace of a call, from what the host knows.
 struct AttnPlan {
-  int mode, groups, ctas, warps;
+  int mode, groups, ctas, warps, per_sm;
   bool pair_mode;
   int64_t bytes;
 };
@@ -1073,30 +1085,33 @@ AttnPlan plan_of(const mk_kv8_cache &c, const mk_batch &b, int n_q_heads, int dt
   const int64_t chunks = ((int64_t)b.max_pages * c.page_size + kChunk - 1) / kChunk;
   p.pair_mode = chunks <= kPairChunks && pairs < (1ll << 30);
   const int sms = sm_count(c.device);
+  const bool crowd = pairs > 4ll * sms && crowd_fits(c.head_dim, p.mode) && (p.pair_mode || c.head_dim == 64);
   if (p.pair_mode) {
     p.ctas = (int)pairs;
     p.warps = pairs <= sms ? 8 : pairs <= 2 * sms ? 4 : 2;
+    p.per_sm = crowd ? kCrowd : ctas_per_sm(p.warps);
     return p;
   }
   p.warps = pairs > 2 * sms ? 2 : p.mode == kRows8F32 || pairs > sms ? 4 : 8;
-  p.ctas = (int)std::min<int64_t>((int64_t)sms * ctas_per_sm(p.warps), (pairs * chunks + kMinUnits - 1) / kMinUnits);
+  p.per_sm = crowd ? kCrowd : ctas_per_sm(p.warps);
+  p.ctas = (int)std::min<int64_t>((int64_t)sms * p.per_sm, (pairs * chunks + kMinUnits - 1) / kMinUnits);
   p.bytes = (int64_t)p.ctas * (32 + 2 * rg * 8 + 2ll * rg * c.head_dim * 4);
   return p;
 }
 
-template <int D, int FMT, int MODE, int W>
+template <int D, int FMT, int MODE, int W, int CTAS>
 cudaError_t launch(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
   constexpr int smem = smem_bytes(D, FMT, MODE, W);
   static std::atomic<uint64_t> ready{0};  // devices whose limit has been raised
   const uint64_t bit = a.c.device < 64 ? 1ull << a.c.device : 0;
   cudaError_t e = cudaSuccess;
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kv8_attention_kernel<D, FMT, MODE, W>,
+    e = cudaFuncSetAttribute(kv8_attention_kernel<D, FMT, MODE, W, CTAS>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  e = pdl_launch(kv8_attention_kernel<D, FMT, MODE, W>, dim3(p.ctas), W * 32, smem, st, a);
+  e = pdl_launch(kv8_attention_kernel<D, FMT, MODE, W, CTAS>, dim3(p.ctas), W * 32, smem, st, a);
   if (e != cudaSuccess || p.pair_mode) return e;
   return pdl_launch(kv8_merge_kernel<D, group_rows(MODE)>, dim3(p.ctas), group_rows(MODE) * 32, 0, st, a,
                     p_log2(FMT, MODE));
@@ -1104,9 +1119,11 @@ cudaError_t launch(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
 
 template <int D, int FMT, int MODE>
 cudaError_t launch(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
-  return p.warps == 2   ? launch<D, FMT, MODE, 2>(a, p, st)
-         : p.warps == 4 ? launch<D, FMT, MODE, 4>(a, p, st)
-                        : launch<D, FMT, MODE, 8>(a, p, st);
+  if constexpr (crowd_fits(D, MODE))
+    if (p.per_sm == kCrowd) return launch<D, FMT, MODE, 2, kCrowd>(a, p, st);
+  return p.warps == 2   ? launch<D, FMT, MODE, 2, 4>(a, p, st)
+         : p.warps == 4 ? launch<D, FMT, MODE, 4, 2>(a, p, st)
+                        : launch<D, FMT, MODE, 8, 1>(a, p, st);
 }
 
 template <int D, int FMT>

@@ -360,3 +360,20 @@ def test_many_failing_sequences_and_rows(wide):
     good = np.setdiff1d(np.arange(n), bad)
     check(out[~fails], lse[~fails], host, 0, q[~fails.cpu()], table[good], cached[good],
           np.concatenate([[0], np.cumsum(new[good])]), 64 ** -0.5, "bfloat16")
+
+
+@pytest.mark.parametrize("dim,fmt,dtype,wide", [(64, "int8", "bfloat16", False), (64, "e4m3", "float32", True),
+                                                (64, "int8", "float32", True), (64, "e4m3", "float16", True),
+                                                (128, "int8", "float16", False), (128, "e4m3", "bfloat16", False)])
+def test_more_pairs_than_ctas(dim, fmt, dtype, wide):
+    rng = np.random.default_rng(dim)
+    cached = rng.integers(0, 70, 340)
+    cached[[3, 200]] = 900
+    if wide:  # longer than a whole CTA's share of the line
+        cached[[17, 339]] = 6000, 2500
+    case = (4, 2, dim, 32, 16, fmt, dtype, list(cached), [1] * 340)
+    host, q, table, cached, new, start = setup(case, 31)
+    cache = host.device()
+    out, lse = cache.attention(1, q.cuda(), dev(table), dev(cached.astype(np.int32)), return_lse=True)
+    cache.check()
+    check(out, lse, host, 1, q, table, cached, start, dim ** -0.5, dtype)
