@@ -362,9 +362,19 @@ class Megakernel:
         """One step, a grid per operator, over an 8-bit paged cache (a KV8Cache with this
         model's layers, kv heads and head_dim) and its int32 page table [batch][max_pages]."""
         import torch
-        if page_table.dim() != 2 or page_table.shape[0] != self.w.batch \
-                or page_table.dtype != torch.int32 or not page_table.is_contiguous():
-            _refuse(f"page_table must be a contiguous int32 tensor [{self.w.batch}][max_pages]")
+        batch = self.w.batch
+        if page_table.dim() != 2 or page_table.shape[0] != batch:
+            _refuse(f"page_table must be [{batch}][max_pages]")
+        cache._int32(page_table, None, "page_table")
+        for t, what in ((tokens_in, "tokens_in"), (tokens_out, "tokens_out"), (kv_len, "kv_len")):
+            cache._int32(t, None, what)
+            if t.numel() < batch:
+                _refuse(f"{what} must have {batch} entries")
+        if logits is not None and (logits.dtype is not torch.float32 or not logits.is_contiguous()
+                                   or logits.get_device() != cache._index
+                                   or logits.numel() < batch * self.w.vocab):
+            _refuse(f"logits must be a contiguous float32 tensor [{batch}][{self.w.vocab}] on "
+                    f"{cache.device}")
         size = ctypes.c_int64()
         max_pages = page_table.shape[1]
         _check(lib().mk_decode_step_kv8_workspace(self._h, cache._ref, max_pages,
