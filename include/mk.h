@@ -389,7 +389,7 @@ enum { MK_F32 = 0, MK_BF16 = 1, MK_F16 = 2 }; /* element types of rows */
 enum {
   MK_CHECK_ROWS = 1,    /* row_start out of order, outside [0, n_rows], or more than max_rows */
   MK_CHECK_LENGTH = 2,  /* kv_len < 0, or kv_len + n above max_pages * page_size */
-  MK_CHECK_PAGE = 3,    /* page table entry outside [0, n_pages) */
+  MK_CHECK_PAGE = 3,    /* page table entry outside [0, n_pages); page calls: or of a page with count 0 */
   MK_CHECK_SEQ = 4,     /* sequence or page number of a list out of range, or named twice */
   MK_CHECK_IN_USE = 5,  /* fork into a sequence that holds pages */
   MK_CHECK_FREE = 6     /* fewer free pages than needed (MK_ERR_OOM; value: how many are lacking) */
@@ -531,7 +531,8 @@ mk_status mk_pages_workspace(const mk_pages *pages, int n, int64_t *bytes);
  * no pages and not be a source.  Device checks: a list entry that is out of
  * range or a destination named twice or as a source (MK_CHECK_SEQ), a
  * destination that holds pages (MK_CHECK_IN_USE), a source entry outside
- * [-1, n_pages) (MK_CHECK_PAGE): the call then changes nothing.
+ * [-1, n_pages) or one that names a free page (MK_CHECK_PAGE): the call then
+ * changes nothing.
  */
 mk_status mk_pages_fork(const mk_pages *pages, int n, const int32_t *d_src, const int32_t *d_dst,
                         void *d_workspace, int64_t workspace_bytes, void *stream);
@@ -539,7 +540,8 @@ mk_status mk_pages_fork(const mk_pages *pages, int n, const int32_t *d_src, cons
 /*
  * mk_pages_free - sequences d_seqs[i], i < n, give their pages back; their
  * entries become -1.  A sequence may be named twice.  Device checks:
- * MK_CHECK_SEQ, MK_CHECK_PAGE (the call then changes nothing).
+ * MK_CHECK_SEQ, MK_CHECK_PAGE (as in mk_pages_fork; the call then changes
+ * nothing).
  */
 mk_status mk_pages_free(const mk_pages *pages, int n, const int32_t *d_seqs, void *d_workspace,
                         int64_t workspace_bytes, void *stream);
@@ -554,7 +556,8 @@ mk_status mk_pages_free(const mk_pages *pages, int n, const int32_t *d_seqs, voi
  * it.
  * Free pages are given lowest number first, in the order of sequence and
  * entry; pages that this call gives up are not given out by it.  Device
- * checks: MK_CHECK_LENGTH, MK_CHECK_PAGE, MK_CHECK_FREE (the call then changes
+ * checks: MK_CHECK_LENGTH, MK_CHECK_PAGE (of the entries that hold these
+ * positions, as in mk_pages_fork), MK_CHECK_FREE (the call then changes
  * nothing).
  */
 mk_status mk_pages_reserve(const mk_pages *pages, const int32_t *d_kv_len, const int32_t *d_n_new,

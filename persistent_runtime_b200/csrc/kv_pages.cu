@@ -149,9 +149,10 @@ __device__ __forceinline__ bool bad_seq(const PageArgs &a, const int32_t *list, 
   return true;
 }
 
-// Entry -1 (no page) or a page of the pools.
+// An entry is -1 (no page) or a page of the pools that is counted: one that names a
+// free page would share it with whoever is given the page next.
 __device__ __forceinline__ bool bad_entry(const PageArgs &a, int s, int page) {
-  if (page >= -1 && page < a.p.n_pages) return false;
+  if (page == -1 || (page >= 0 && page < a.p.n_pages && a.p.d_ref[page] >= 1)) return false;
   record_status(a.p.d_status, MK_ERR_DEVICE, s, page, MK_CHECK_PAGE);
   return true;
 }
@@ -395,10 +396,6 @@ __global__ void __launch_bounds__(kTeamThreads) compact_kernel(const __grid_cons
   for (int64_t e = t.index(); e < entries; e += t.threads()) {
     const int page = a.p.d_page_table[e], s = (int)(e / a.p.max_pages);
     if (bad_entry(a, s, page)) bad = true;
-    else if (page >= 0 && a.p.d_ref[page] < 1) {
-      bad = true;
-      record_status(a.p.d_status, MK_ERR_DEVICE, s, page, MK_CHECK_PAGE);
-    }
   }
   if (t.any(bad)) return;
   int p0, p1;
