@@ -459,13 +459,17 @@ mk_status mk_kv8_store(const mk_kv8_cache *cache, int layer, const mk_rows *k, c
  * [head_dim], contiguous, 16-byte aligned and apart from q, has its element type;
  * d_lse [n_rows][n_q_heads] (or NULL) receives log(sum(exp(scores))).  Rows
  * outside every sequence are not written.  Codes enter the products exactly,
- * sums and softmax are fp32 (int8 products: exact integers).  A query element
- * enters with an error of at most 2^-21 of its row's largest (int8) or 2^-12
- * of itself (e4m3; fp32 rows 2^-23), a probability with 2^-17 of the largest of
- * its chunk of 32 positions (int8; fp32 rows 2^-24) or 2^-12 of itself (e4m3;
- * fp32 rows 2^-22; very small ones instead with 2^-24 of the row's largest
- * element and 2^-39 of the chunk's largest probability).  max_rows is at most
- * MK_KV8_MAX_ROWS: the call is made for decoding, not for prompts.
+ * sums and softmax are fp32 (int8 products: exact integers).  An exponential is
+ * off by 2 ulp.  Besides that a query element enters the products with an error
+ * of at most
+ *   int8    2^-20.8 of its row's largest,
+ *   e4m3    none (16-bit rows) or 2^-23 of itself (fp32 rows), but elements below
+ *           2^-13 of the row's largest 2^-24 (fp32 rows 2^-35) of that,
+ * and a probability with
+ *   int8    2^-16.9 (fp32 rows 2^-24) of the largest of its chunk of 32 positions,
+ *   e4m3    2^-11 (fp32 rows 2^-22) of itself, or 2^-39 of its chunk's largest.
+ * max_rows is at most MK_KV8_MAX_ROWS: the call is made for decoding, not for
+ * prompts.
  * Workspace: at least mk_kv8_attention_workspace bytes, 16-byte aligned; its
  * contents need not be initialised.  Results do not depend on how the work is
  * spread over time: the same call gives the same bits.

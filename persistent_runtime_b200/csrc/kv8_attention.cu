@@ -146,10 +146,12 @@ __host__ __device__ constexpr int p_terms(int fmt, int mode) {
   return (fmt == MK_KV8_INT8 ? 2 : 1) + (mode == kRows8F32 ? 1 : 0);
 }
 
-// log2 of the factor that P carries, relative to its chunk's maximum: int8, 16
-// bits (the maximum is 65535) or 24 (2^23); fp16: normal down to 2^-28.
-__host__ __device__ constexpr float p_log2(int fmt, int mode) {
-  return fmt != MK_KV8_INT8 ? 14.0f : mode == kRows8F32 ? 23.0f : 15.99997798605f;
+// The factor that P carries in the products, relative to its chunk's maximum:
+// int8, 16 bits (the maximum is 65535) or 24 (2^23); fp16: normal down to 2^-28.
+// The exponentials are multiplied by it: added to their arguments, its logarithm
+// would leave these 19 to 21 bits behind the point.
+__host__ __device__ constexpr float p_factor(int fmt, int mode) {
+  return fmt != MK_KV8_INT8 ? 16384.0f : mode == kRows8F32 ? 8388608.0f : 65535.0f;
 }
 
 // Shared memory: for each warp a slot for a chunk's K codes and scales and one
@@ -707,15 +709,16 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
         uint32_t r0[2], r1[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          constexpr float kUp = p_log2(FMT, MODE);
-          const float p0 = exp2_fast((x[j][tl][2 * r] - ref[0]) + kUp);
-          const float p1 = exp2_fast((x[j][tl][2 * r + 1] - ref[1]) + kUp);
-          sum[0] += p0;
-          sum[1] += p1;
+          constexpr float kUp = p_factor(FMT, MODE);
+          const float e0 = exp2_fast(x[j][tl][2 * r] - ref[0]);
+          const float e1 = exp2_fast(x[j][tl][2 * r + 1] - ref[1]);
+          sum[0] += e0;
+          sum[1] += e1;
+          const float p0 = e0 * kUp, p1 = e1 * kUp;
           if constexpr (INT && NP == 2) {
             // adding 2^23 rounds to an integer in the low bits
-            r0[r] = transpose8x8(__byte_perm(__float_as_uint(p0 + 8388608.0f),
-                                             __float_as_uint(p1 + 8388608.0f), 0x5410));
+            r0[r] = transpose8x8(__byte_perm(__float_as_uint(fmaf(e0, kUp, 8388608.0f)),
+                                             __float_as_uint(fmaf(e1, kUp, 8388608.0f)), 0x5410));
           } else if constexpr (INT) {
             const uint32_t n0 = __float2uint_rn(p0), n1 = __float2uint_rn(p1);
             r0[r] = transpose8x8(__byte_perm(n0, n1, 0x6521));
@@ -820,9 +823,9 @@ __device__ __forceinline__ void run_segment(const AttnArgs &a, uint8_t *smem, co
     if (whole) {
       const int i = a.by_rep.quotient(r);
       const int64_t row = (int64_t)(q.r0 + i) * a.n_q_heads + hk * rep + r - i * rep;
-      const float by = 1.0f / sum;
+      const float by = 1.0f / (sum * p_factor(FMT, MODE));
       store_places<D>(a.out, a.q.dtype, row * D, d, acc.x * by, acc.y * by, acc.z * by, acc.w * by);
-      if (a.lse && d == 0) a.lse[row] = (top - p_log2(FMT, MODE) + log2f(sum)) * kLn2;
+      if (a.lse && d == 0) a.lse[row] = (top + log2f(sum)) * kLn2;
     } else {
       *reinterpret_cast<float4 *>(a.part + ((int64_t)slot * RG + col) * D + d) = acc;
       if (d == 0) *reinterpret_cast<float2 *>(a.ml + ((int64_t)slot * RG + col) * 2) = make_float2(top, sum);
@@ -995,7 +998,7 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv8_attention_kernel(const __gri
 // row: its partial results lie in that CTA's slot 2 c + 1 and in the slots 2 c'
 // of the CTAs c' behind it, and are added in that order.
 template <int D, int RG>
-__global__ void __launch_bounds__(RG * 32) kv8_merge_kernel(const __grid_constant__ AttnArgs a, float p_log2) {
+__global__ void __launch_bounds__(RG * 32) kv8_merge_kernel(const __grid_constant__ AttnArgs a, float p_factor) {
   pdl_trigger();
   pdl_wait();
   if (gated(a.gate)) return;
@@ -1057,10 +1060,10 @@ __global__ void __launch_bounds__(RG * 32) kv8_merge_kernel(const __grid_constan
   }
   const int i = a.by_rep.quotient(r), h = cut.y * a.by_rep.d + r - i * a.by_rep.d;
   const int64_t row = (int64_t)(rows.x + i) * a.n_q_heads + h;
-  const float by = 1.0f / sum;
+  const float by = 1.0f / (sum * p_factor);
 #pragma unroll
   for (int d = 0; d < N; d += 2) store2(a.out, a.q.dtype, row * D + dim_of<D>(lane * N + d), acc[d] * by, acc[d + 1] * by);
-  if (a.lse && lane == 0) a.lse[row] = (top - p_log2 + log2f(sum)) * kLn2;
+  if (a.lse && lane == 0) a.lse[row] = (top + log2f(sum)) * kLn2;
 }
 
 int mode_of(int dtype, int rep, int max_rows) {
@@ -1114,7 +1117,7 @@ cudaError_t launch(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
   e = pdl_launch(kv8_attention_kernel<D, FMT, MODE, W, CTAS>, dim3(p.ctas), W * 32, smem, st, a);
   if (e != cudaSuccess || p.pair_mode) return e;
   return pdl_launch(kv8_merge_kernel<D, group_rows(MODE)>, dim3(p.ctas), group_rows(MODE) * 32, 0, st, a,
-                    p_log2(FMT, MODE));
+                    p_factor(FMT, MODE));
 }
 
 template <int D, int FMT, int MODE>
