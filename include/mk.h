@@ -470,6 +470,8 @@ mk_status mk_kv8_store(const mk_kv8_cache *cache, int layer, const mk_rows *k, c
  *   e4m3    2^-11 (fp32 rows 2^-22) of itself, or 2^-39 of its chunk's largest.
  * max_rows is at most MK_KV8_MAX_ROWS: the call is made for decoding, not for
  * prompts.
+ * Scores and the unnormalised sum of probabilities times values, the largest
+ * probability being 1, have to stay in the range of fp32.
  * Workspace: at least mk_kv8_attention_workspace bytes, 16-byte aligned; its
  * contents need not be initialised.  Results do not depend on how the work is
  * spread over time: the same call gives the same bits.

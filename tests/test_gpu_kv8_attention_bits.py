@@ -53,3 +53,42 @@ def test_scores_a_little_below_the_largest(fmt, dtype):
     if dtype == "float32":
         got = out.double().cpu().numpy()[:, 0]
         assert (np.abs(got * total[:, None] - 1.0)).max() <= 7.4 * u
+
+
+RANGE_CASES = [
+    # q heads, kv heads, dim, page, block, cached, new rows
+    (4, 2, 64, 64, 16, [40, 333], [1, 1]),             # whole pairs
+    (8, 1, 128, 64, 64, [5000, 700], [1, 2]),          # cut ones
+    (16, 1, 64, 32, 16, [900, 30], [3, 1]),            # sixteen rows
+]
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("case", RANGE_CASES, ids=["whole", "cut", "rows16"])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_large_and_small_values(case, fmt, dtype):
+    """Values times a power of two give the output times that power, bit for bit, as long as the
+    values' sum and the scales stay in fp32's normal range: each operation commutes with it."""
+    import kv8_ref as ref
+    t = torch()
+    Hq, H, D, P, T, cached, new = case
+    cached, new = np.array(cached), np.array(new)
+    table, n_pages = ref.make_table(cached + new, P, seed=3)
+    host = ref.Cache(n_pages, 1, H, D, P, T, fmt, 5)
+    start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = t.from_numpy(np.random.default_rng(6).standard_normal((start[-1], Hq, D)).astype(np.float32))
+    args = (q.to(getattr(t, dtype)).cuda(), dev(table), dev(cached.astype(np.int32)))
+
+    def run(power):
+        cache = host.device()
+        cache.v_scale *= 2.0 ** power
+        out, lse = cache.attention(0, *args, row_start=dev(start), max_rows=int(new.max()), return_lse=True)
+        cache.check()
+        return out.double(), lse
+
+    want, want_lse = run(0)
+    # e4m3 values are up to 448 (0.7 + 0.6) / 90 = 6.5, int8 1.9; 5001 of them sum to 2^15 at most
+    for power in (112, 100, 60, -60, -90):
+        out, lse = run(power)
+        assert t.equal(out, want * 2.0 ** power), power
+        assert t.equal(lse, want_lse)
