@@ -220,8 +220,6 @@ __global__ void __launch_bounds__(256) kv8_store_kernel(const __grid_constant__ 
   for (int p = 0; p < PASSES; ++p) top = v[p].max_bits(top);
   if constexpr (DT != MK_F32) top = max(top & 0xffffu, top >> 16);
   top = __reduce_max_sync(0xffffffffu, top);
-  // Also where a warp has the block to itself: all lanes have read the old
-  // scale before it is written.
   __shared__ uint32_t tops[8];
   if (a.split_log2 > 0) {
     if (lane == 0) tops[warp] = top;
@@ -259,6 +257,9 @@ __global__ void __launch_bounds__(256) kv8_store_kernel(const __grid_constant__ 
     }
     dst += dst_step;
   }
+  // All lanes have read the old scale: other warps' before the barrier above, this one's
+  // before this one (the reduction orders no memory).
+  __syncwarp();
   if (on && lane == 0 && sub == 0) *scale = nan ? __int_as_float(0x7fc00000) : sc;
 }
 
