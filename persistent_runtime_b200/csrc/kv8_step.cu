@@ -182,7 +182,10 @@ extern "C" mk_status mk_decode_step_kv8(mk_handle *h, const int32_t *d_tokens_in
   if (ops_workspace("mk_decode_step_kv8", d_workspace, workspace_bytes, w.total) != MK_OK)
     return refuse(h, MK_ERR_ARG, mk_last_error(nullptr));
   DeviceGuard guard(h->device);
-  if (guard.error() != cudaSuccess) return refuse(h, MK_ERR_CUDA, cudaGetErrorString(guard.error()));
+  if (guard.error() != cudaSuccess) {
+    ops_cuda_fail(guard.error(), "mk_decode_step_kv8");
+    return refuse(h, MK_ERR_CUDA, cudaGetErrorString(guard.error()));
+  }
 
   const mk_model_config &m = h->cfg;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -232,8 +235,8 @@ extern "C" mk_status mk_decode_step_kv8(mk_handle *h, const int32_t *d_tokens_in
       }
     }
     if (e != cudaSuccess) {
-      h->err = cudaGetErrorString(e);
-      return MK_ERR_CUDA;
+      ops_cuda_fail(e, "mk_decode_step_kv8");
+      return refuse(h, MK_ERR_CUDA, cudaGetErrorString(e));
     }
   }
   return MK_OK;

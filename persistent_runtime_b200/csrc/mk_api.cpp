@@ -698,6 +698,7 @@ mk_status mk::ops_fail(mk_status s, const char *call, const char *text) noexcept
 }
 
 mk_status mk::ops_cuda_fail(cudaError_t e, const char *call) noexcept {
+  cudaGetLastError();  // reported here: not once more by the next launch that asks for it
   return ops_fail(MK_ERR_CUDA, call, cudaGetErrorString(e));
 }
 
@@ -720,7 +721,10 @@ int mk::sm_count(int device) {
   const bool keep = device >= 0 && device < 64;
   int n = keep ? known[device].load(std::memory_order_relaxed) : 0;
   if (n > 0) return n;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return 1;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
+    cudaGetLastError();
+    return 1;
+  }
   if (keep) known[device].store(n, std::memory_order_relaxed);
   return n;
 }
