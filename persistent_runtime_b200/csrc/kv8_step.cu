@@ -110,8 +110,11 @@ __global__ void attention_operand(const float *att, uint16_t *opnd, int K, int n
   opnd[at + 4] = to_bf(x - bf(hi));
 }
 
-mk_status refuse(mk_handle *h, mk_status s, const char *text) {
-  h->err = text;
+mk_status refuse(mk_handle *h, mk_status s, const char *text) noexcept {
+  try {
+    h->err = text;
+  } catch (...) {  // no memory for the text: the status still says what happened
+  }
   return s;
 }
 
