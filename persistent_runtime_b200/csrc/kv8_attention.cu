@@ -1166,7 +1166,8 @@ const char *check_heads(const mk_kv8_cache *c, int n_q_heads, int dtype, const m
   const int64_t chunks = ((int64_t)b->max_pages * c->page_size + kChunk - 1) / kChunk + pair_units(kRows16);
   const int64_t groups = ((int64_t)n_q_heads / c->n_kv_heads * b->max_rows + 7) / 8;
   if ((int64_t)c->n_kv_heads * groups >= (1 << 21)) return "so many heads and rows are not supported";
-  if (chunks * c->n_kv_heads * groups * b->n_seqs >= (1ll << 30))
+  // chunks < 2^27, heads x groups < 2^21, sequences <= 2^24: no product of all three
+  if (chunks * (c->n_kv_heads * groups) > ((1ll << 30) - 1) / b->n_seqs)
     return "so many positions (page table entries x heads) are not supported";
   return nullptr;
 }
