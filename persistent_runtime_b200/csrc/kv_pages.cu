@@ -565,6 +565,7 @@ const char *check_pages(const mk_pages *p) {
   for (int i = 0; i < p->n_pools; ++i) {
     if (!p->d_pool[i] || (reinterpret_cast<uintptr_t>(p->d_pool[i]) & 3)) return "a pool is null or not 4-byte aligned";
     if (p->page_bytes[i] < 4 || (p->page_bytes[i] & 3)) return "page_bytes must be a positive multiple of 4";
+    if (p->page_bytes[i] >= (1ll << 40)) return "page_bytes out of range";  // before they are added
     bytes += p->page_bytes[i];
     steps += (p->page_bytes[i] + kCopyBytes - 1) / kCopyBytes;
   }
