@@ -637,6 +637,8 @@ class KV8Cache(_Status):
                 or not out.is_contiguous() or out.data_ptr() == q.data_ptr():
             _refuse("out must be contiguous, with the shape, type and device of q, and not q itself")
         lse = self._floats(n_rows, n_heads) if return_lse else None
+        if n == n_rows == 0:
+            return (out, lse) if return_lse else out
         rq, _, b = self._at
         # the workspace's size follows from the sizes alone
         key = (n_heads, q.dtype, n, max_rows, max_pages)
