@@ -681,6 +681,8 @@ class PagePool(_Status):
         self.pools = list(pools)
         self._new_status()
         n_pages = ref_count.numel()
+        if n_pages < 1:
+            _refuse("ref_count must have an entry for every page")
         p = self._c = Pages(page_table.device.index, n_pages, page_table.shape[0],
                             page_table.shape[1], page_size, len(pools))
         for i, x in enumerate(self.pools):
@@ -700,6 +702,8 @@ class PagePool(_Status):
     def empty(cls, n_seqs, max_pages, page_size, pools):
         """Nobody holds a page yet."""
         import torch
+        if not len(pools):
+            _refuse("no pools")
         device = pools[0].device
         return cls(torch.full((n_seqs, max_pages), -1, dtype=torch.int32, device=device),
                    torch.zeros(pools[0].shape[0], dtype=torch.int32, device=device), page_size,

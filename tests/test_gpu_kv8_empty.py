@@ -31,3 +31,16 @@ def test_a_batch_without_sequences():
         cache.attention(0, some, table, lens, row_start=start, max_rows=1)
     with pytest.raises(prb.MkError):
         cache.store(0, some[:, :2], some[:, :2], table, lens, row_start=start)
+
+
+def test_pools_without_pages_are_refused():
+    import persistent_runtime_b200 as prb
+    t = torch()
+    none, table = t.zeros(0, dtype=t.int32, device="cuda"), t.zeros(2, 2, dtype=t.int32, device="cuda")
+    for pools in ([], [t.zeros(0, 4, device="cuda")]):
+        with pytest.raises(prb.MkError):
+            prb.PagePool(table, none, 16, pools)
+    with pytest.raises(prb.MkError):
+        prb.PagePool.empty(2, 2, 16, [])
+    with pytest.raises(prb.MkError):
+        prb.PagePool.empty(2, 2, 16, [t.zeros(0, 4, device="cuda")])
