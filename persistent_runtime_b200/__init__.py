@@ -499,7 +499,9 @@ class KV8Cache(_Status):
 
     The pages belong to sequences as in Megakernel.decode_steps_paged: position p of sequence s
     is row p % page_size of page page_table[s][p // page_size].  Calls are asynchronous on the
-    current (or the given) stream of the cache's device; use one object per thread."""
+    current (or the given) stream of the cache's device; use one object per thread.  With
+    `stream` the caller's tensors must be ready on that stream, and stay alive (or be recorded
+    there with Tensor.record_stream) until the call has run; what a call returns is recorded."""
 
     def __init__(self, k, v, k_scale, v_scale):
         import torch
@@ -611,8 +613,9 @@ class KV8Cache(_Status):
                   out=None, return_lse=False, stream=None):
         """mk_kv8_attention: q [n_rows][n_q_heads][head_dim]; row i of sequence s sees the
         positions 0 to kv_len[s] + i.  max_rows bounds the rows of one sequence (1 without
-        row_start; at most MK_KV8_MAX_ROWS).  Returns the output in q's type, and with
-        return_lse also the float32 log-sum-exp [n_rows][n_q_heads]."""
+        row_start; at most MK_KV8_MAX_ROWS).  Returns the output in q's type (in `out` if given,
+        which must not overlap q), and with return_lse also the float32 log-sum-exp
+        [n_rows][n_q_heads]."""
         if stream is not None:
             import torch
             now = torch.cuda.current_stream(self.device)
@@ -669,7 +672,7 @@ class PagePool(_Status):
     pools       tensors whose first dimension are the pages: the K and V pools of
                 Megakernel.decode_steps_paged, or KV8Cache.pools()
 
-    Calls are asynchronous, like KV8Cache's; use one object per thread."""
+    Calls are asynchronous and take a stream as KV8Cache's do; use one object per thread."""
 
     def __init__(self, page_table, ref_count, page_size, pools):
         self._bind(page_table.device)
