@@ -115,19 +115,20 @@ constexpr int group_rows(int mode) { return mode == kRows16 ? 16 : 8; }
 
 // A CTA has 8 warps and an SM to itself, 4 warps and half of one, or 2 and a
 // quarter: the registers of 8 warps are an SM's.  Few pairs: 8 (one long sequence
-// of e4m3 53 us against 59 with 4), with fp32 rows and cut lines 4 (batch 8 22.5
-// against 26 at that time).  More pairs than SMs: 4, more than twice as many: 2,
-// because what a pair costs besides its chunks then overlaps with other pairs' (64
-// sequences of 250: 20.6, 13.2 and 11.0 us with 8, 4 and 2).
+// of e4m3 52.0 us against 54.9 with 4), with fp32 rows and cut lines 4 (batch 8 13.8
+// against 14.8; 16 sequences of 8192 50.6 against 56.3, of 1023 14.3 against 13.2).
+// More pairs than SMs: 4, more than twice as many: 2, because what a pair costs
+// besides its chunks then overlaps with other pairs' (64 sequences of 250: 17.7, 12.7
+// and 10.5 us with 8, 4 and 2).
 __host__ __device__ constexpr int ctas_per_sm(int warps) { return 8 / warps; }
 
 // More pairs than four CTAs per SM: six CTAs of 2 warps, in 168 registers a thread,
 // where the code fits with few spills or none.  head_dim 64 (16 bf16 heads on 8,
-// int8): 96 sequences of 1000 36.6 -> 25.3 us, 112 to 512 of 250 12.6 -> 12.2 and 45.8
-// -> 37.1, 128 of up to 4000 68.6 -> 59.1.  head_dim 128 with 16-bit rows (32 heads on
-// 8): only for short page tables, 96 sequences of 250 17.7 -> 12.4 us, 512 65.0 -> 58.3
-// (128, which fill six CTAs just over once, 18.0 -> 18.9); long pairs run at the HBM
-// rate and would lose by the spills (96 of up to 4000 72.3 -> 75.5).
+// int8): 96 sequences of 1000 37.7 -> 25.5 us, 112 and 512 of 250 13.1 -> 12.4 and 46.0
+// -> 36.8, 128 of up to 4000 68.9 -> 58.9.  head_dim 128 with 16-bit rows (32 heads on
+// 8): only for short page tables, 96 sequences of 250 18.8 -> 13.1 us, 512 65.0 -> 58.0
+// (128, which fill six CTAs just over once, lose: 19.7 -> 21.9); long pairs run at the
+// HBM rate and would lose by the spills (96 of up to 4000 72.3 -> 75.5 when it was tried).
 constexpr int kCrowd = 6;
 __host__ __device__ constexpr bool crowd_fits(int D, int mode) {
   return mode == kRows8 || (D == 64 && mode == kRows8F32);
@@ -139,7 +140,12 @@ __host__ __device__ constexpr int pair_units(int mode) { return mode == kRows16 
 
 // Terms of a query element in the MMAs (int8: three signed 7-bit digits, fp16:
 // one or, for fp32 rows, two numbers) and of a probability (8-bit digits; fp16
-// numbers).
+// numbers).  16-bit rows make do with a term less of a probability: with one more,
+// outputs differ from those of fp32 probabilities by at most 5e-5 instead of 2.4e-4 to
+// 8e-4 (norm of the difference over that of the output), which their rounding to 16
+// bits covers (error against 64 bits of bf16 outputs 1.6e-3 both ways; of fp16 rows on
+// e4m3 2.1e-4 instead of 2.4e-4), and take longer: 16 x 8192 int8 49.9 -> 56.0 us, e4m3
+// 47.8 -> 50.2, 7 x 6001 of five fp16 rows 14.6 -> 16.1, 1024 x 100 68.7 -> 75.9.
 __host__ __device__ constexpr int q_terms(int fmt, int mode) {
   return fmt == MK_KV8_INT8 ? 3 : mode == kRows8F32 ? 2 : 1;
 }
@@ -969,8 +975,8 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv8_attention_kernel(const __gri
   const int per = max(kMinUnits, a.by_grid.quotient(total + (int)gridDim.x - 1));
   // Whole pairs where the busiest CTA's share is at most 4/3 of an equal one and
   // a bit: an SM alone draws 4/3 of its share of the HBM rate, and cutting
-  // costs partial results and their sums (16 sequences of 1024: 14.6 us whole,
-  // 18.5 cut; 8 of 256 to 4096: 34.9 whole, 16.5 cut).
+  // costs partial results and their sums (16 sequences of 1023: 12.1 us whole,
+  // 15.8 cut; 8 of 256 to 4096: 25.5 whole, 14.0 cut).
   const int64_t busiest = (int64_t)a.by_grid.quotient(pairs + (int)gridDim.x - 1) * (longest + pair_units(MODE));
   whole = 3 * busiest <= 4 * ((int64_t)per + kCutUnits);
   const int u0 = whole ? (int)blockIdx.x : (int)min((int64_t)total, (int64_t)per * blockIdx.x);

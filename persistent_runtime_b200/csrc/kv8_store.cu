@@ -9,7 +9,7 @@
 // step.  The warps of a CTA take neighbouring heads of the same rows, which lie
 // next to each other in the usual [rows][heads][head_dim]: 98k bf16 rows of 8
 // heads (604 MB) took 347 us with a CTA per head, 156 us with a CTA that went
-// through the heads one after the other, 143 us side by side and 105 us (5.8 TB/s)
+// through the heads one after the other, 143 us side by side and 102 us (5.9 TB/s)
 // with packed products and no divisions.  Eight octets of a lane instead of 16
 // (twice the warps for a block) were slower, 137 against 116 us.
 //

@@ -14,11 +14,13 @@
 // The copy is bound by HBM: every moved byte is read and written once, or, where
 // one page is copied for several sequences, read once: their copies lie next to
 // each other in the list and the later reads hit L2.  About 100 pages of
-// an 8B decoder's 8-bit pools (4.7 MB each) move in 142 us (6.5 TB/s); 32 pages
-// copied three times each take 116 us with the bookkeeping.  The grid is the CTAs that are resident
-// (a call that moves nothing should cost a launch, not thousands of empty CTAs:
-// 64 CTAs per SM cost 9 us more) and takes steps as it goes: SMs differ in their
-// distance to memory, and equal shares took 7 % longer.
+// an 8B decoder's 8-bit pools (4.7 MB each) move in 143 us (6.5 TB/s); 32 pages
+// copied three times each take 119 us with the bookkeeping, where one read and
+// three writes at the copy's rate would be 89: the repeated reads go through L2.
+// The grid is the CTAs that are resident (a call that moves nothing should cost a
+// launch, not thousands of empty CTAs: 64 CTAs per SM cost 9 us more) and takes
+// steps as it goes: SMs differ in their distance to memory, and equal shares took
+// 7 % longer.
 #include <cooperative_groups.h>
 
 #include <algorithm>
